@@ -84,11 +84,14 @@ def draw(rng):
 
 # ---------------------------------------------------------------- inputs
 def _quantise_mxfp8(v):
-    """MXFP8 rows of v [rows, d] as one byte buffer: codes [rows, d], then scales [rows, d/32]."""
-    b = v.float().reshape(-1, 32)
-    s = (((b.abs().amax(1).view(torch.int32) >> 23) & 255) - 8).clamp_min(0)
-    q = (b * torch.exp2((127 - s).double()).float()[:, None]).clamp(-448, 448).to(torch.float8_e4m3fn)
-    return torch.cat([q.view(torch.uint8).reshape(-1), s.to(torch.uint8)])
+    """MXFP8 rows of v [rows, d] as one byte buffer: codes [rows, d], then the rows' d/32 scales, each
+    row of them filled up to a multiple of 4 bytes."""
+    rows, d = v.shape
+    b = v.float().reshape(rows, d // 32, 32)
+    s = (((b.abs().amax(2).view(torch.int32) >> 23) & 255) - 8).clamp_min(0)
+    q = (b * torch.exp2((127 - s).double()).float()[..., None]).clamp(-448, 448).to(torch.float8_e4m3fn)
+    s = torch.nn.functional.pad(s.to(torch.uint8), (0, -(d // 32) % 4))
+    return torch.cat([q.view(torch.uint8).reshape(-1), s.reshape(-1)])
 
 
 def _random_entries(n, d, f, g):
@@ -179,7 +182,8 @@ def _mxfp4(v):
 
 def _rows_of(x8, rows, d):
     q = x8[:rows * d].view(torch.float8_e4m3fn).float().reshape(rows, d // 32, 32)
-    return (q * torch.exp2(x8[rows * d:].float() - 127).reshape(rows, d // 32, 1)).reshape(rows, d)
+    s = torch.exp2(x8[rows * d:].float() - 127).reshape(rows, -1, 1)[:, :d // 32]
+    return (q * s).reshape(rows, d)
 
 
 def _matrix_of(entries, part, R, K):
@@ -358,7 +362,7 @@ def exact(case, seed):
                 "y8": _exact_mx(y, E4M3) if case["mx8"] else None}
     k, f = case["k"], case["f"]
     x = st["x8"][:T * d].view(torch.float8_e4m3fn).double().view(T, d)
-    x = x * torch.exp2(st["x8"][T * d:].double() - 127).repeat_interleave(32).view(T, d)
+    x = x * torch.exp2(st["x8"][T * d:].double().view(T, -1)[:, :d // 32] - 127).repeat_interleave(32, 1)
     values = torch.tensor(E2M1 + tuple(-v for v in E2M1), dtype=torch.float64, device="cuda")
     at, y = st["offsets"].tolist(), torch.empty((T * k, d), dtype=torch.float64, device="cuda")
     for e in range(case["E"]):
