@@ -27,6 +27,7 @@ MOE_ETIMEOUT = -7
 MOE_F32 = 0
 MOE_BF16 = 1
 MOE_MXFP4 = 2
+MOE_MXFP8 = 3
 
 MOE_PATH_AUTO = 0
 MOE_PATH_GEMV = 1
@@ -37,6 +38,8 @@ EXPORTS = [
     "moe_permute_workspace_bytes", "moe_permute", "moe_route_permute", "moe_entry_bytes",
     "moe_expert_ffn_workspace_bytes",
     "moe_expert_ffn", "moe_expert_ffn_noalloc", "moe_expert_ffn_noalloc_max_bytes",
+    "moe_entry_quantize", "moe_entry_dequantize", "moe_mxfp8_bytes", "moe_mxfp8_quantize",
+    "moe_mxfp8_dequantize", "moe_rmsnorm", "moe_combine_rmsnorm",
     "moe_combine", "moe_decode_token_workspace_bytes", "moe_decode_token", "cache_init", "cache_lookup_update",
     "cache_lookup_update_split", "cache_fill",
     "cache_fill_device", "cache_fill_masks", "cache_resize", "layer_stream_prefetch", "moe_hbm_read_probe", "moe_copy_probe",
@@ -76,6 +79,7 @@ def lib():
             _build.build()
         L = ctypes.CDLL(path)
         i32, vp, sz, cp = ctypes.c_int, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_char_p
+        f32 = ctypes.c_float
         sig = {
             "moe_strerror": ([i32], cp),
             "moe_abi_version": ([], i32),
@@ -91,6 +95,14 @@ def lib():
             "moe_expert_ffn_noalloc": ([vp, i32, vp, vp, i32, i32, i32, i32, i32, vp, vp, sz, i32,
                                         vp, vp, i32, vp, i32, i32, vp, vp], i32),
             "moe_expert_ffn_noalloc_max_bytes": ([], sz),
+            "moe_entry_quantize": ([vp, i32, sz, i32, i32, i32, vp, sz, vp], i32),
+            "moe_entry_dequantize": ([vp, sz, i32, i32, i32, vp, i32, sz, vp], i32),
+            "moe_mxfp8_bytes": ([i32, i32], sz),
+            "moe_mxfp8_quantize": ([vp, i32, i32, i32, vp, vp], i32),
+            "moe_mxfp8_dequantize": ([vp, i32, i32, vp, i32, vp], i32),
+            "moe_rmsnorm": ([vp, i32, vp, i32, vp, i32, f32, i32, i32, vp, vp, i32, vp, vp], i32),
+            "moe_combine_rmsnorm": ([vp, i32, vp, vp, i32, vp, i32, vp, i32, f32, i32, i32, vp, vp,
+                                     i32, vp, vp], i32),
             "moe_combine": ([vp, i32, vp, vp, i32, i32, i32, vp, vp], i32),
             "moe_decode_token_workspace_bytes": ([i32, i32], sz),
             "moe_decode_token": ([vp, vp, i32, i32, i32, i32, vp, vp, sz, i32, vp, i32, vp, vp, vp,
@@ -209,6 +221,43 @@ def moe_expert_ffn_noalloc(x, act_dtype, perm, offsets, T, k, E, d, f, expert_sl
 
 def moe_expert_ffn_noalloc_max_bytes():
     return lib().moe_expert_ffn_noalloc_max_bytes()
+
+
+def moe_entry_quantize(src, src_dtype, src_stride, n, d, f, dst, dst_stride, stream=None):
+    _check("moe_entry_quantize", lib().moe_entry_quantize(_p(src), src_dtype, src_stride, n, d, f,
+                                                          _p(dst), dst_stride, _s(stream)))
+
+
+def moe_entry_dequantize(src, src_stride, n, d, f, dst, dst_dtype, dst_stride, stream=None):
+    _check("moe_entry_dequantize", lib().moe_entry_dequantize(_p(src), src_stride, n, d, f, _p(dst),
+                                                              dst_dtype, dst_stride, _s(stream)))
+
+
+def moe_mxfp8_bytes(T, d):
+    return lib().moe_mxfp8_bytes(T, d)
+
+
+def moe_mxfp8_quantize(x, x_dtype, T, d, x8, stream=None):
+    _check("moe_mxfp8_quantize", lib().moe_mxfp8_quantize(_p(x), x_dtype, T, d, _p(x8), _s(stream)))
+
+
+def moe_mxfp8_dequantize(x8, T, d, x, x_dtype, stream=None):
+    _check("moe_mxfp8_dequantize", lib().moe_mxfp8_dequantize(_p(x8), T, d, _p(x), x_dtype,
+                                                              _s(stream)))
+
+
+def moe_rmsnorm(x, x_dtype, delta, delta_dtype, gamma, gamma_dtype, eps, T, d, x_out, y, y_dtype,
+                y8, stream=None):
+    _check("moe_rmsnorm", lib().moe_rmsnorm(
+        _p(x), x_dtype, _p(delta), delta_dtype, _p(gamma), gamma_dtype, eps, T, d, _p(x_out), _p(y),
+        y_dtype, _p(y8), _s(stream)))
+
+
+def moe_combine_rmsnorm(y_perm, y_perm_dtype, inv, topk_w, k, x, x_dtype, gamma, gamma_dtype, eps,
+                        T, d, x_out, y, y_dtype, y8, stream=None):
+    _check("moe_combine_rmsnorm", lib().moe_combine_rmsnorm(
+        _p(y_perm), y_perm_dtype, _p(inv), _p(topk_w), k, _p(x), x_dtype, _p(gamma), gamma_dtype,
+        eps, T, d, _p(x_out), _p(y), y_dtype, _p(y8), _s(stream)))
 
 
 def moe_combine(y_perm, y_dtype, inv, topk_w, T, k, d, out, stream=None):

@@ -21,6 +21,7 @@
 #include <mutex>
 
 #include "ffn_args.h"
+#include "mx8_dev.h"
 
 using namespace moe;
 
@@ -98,6 +99,7 @@ extern "C" size_t moe_entry_bytes(int d, int f, int w_dtype) {
 
 // The SwiGLU intermediate h, T*k rows of f units: what every path needs at least.
 static size_t ffn_h_bytes(int T, int k, int f, int act_dtype) {
+  if (act_dtype == MOE_MXFP8) return (size_t)T * k * ((size_t)f + mxfp8_scale_stride(f));
   return (size_t)T * k * f * (act_dtype == MOE_F32 ? 4 : 2);
 }
 
@@ -105,6 +107,7 @@ static size_t ffn_h_bytes(int T, int k, int f, int act_dtype) {
 // per unit), which lets MXFP4 calls run both projections in one launch.
 extern "C" size_t moe_expert_ffn_workspace_bytes(int T, int k, int f, int act_dtype) {
   if (T <= 0 || k <= 0 || f <= 0) return 256;
+  if (act_dtype == MOE_MXFP8) return (ffn_h_bytes(T, k, f, act_dtype) + 255) / 256 * 256;
   const size_t el = act_dtype == MOE_F32 ? 4 : T <= kMxMaxRows ? 4 : 2;
   return ((size_t)T * k * f * el + 255) / 256 * 256;
 }
@@ -123,7 +126,8 @@ extern "C" int moe_expert_ffn(const void* x, int act_dtype, const int32_t* perm,
   if (f32) {
     if (act_dtype != MOE_F32 || y_dtype != MOE_F32) return MOE_EUNSUPPORTED;
   } else if (w_dtype == MOE_BF16 || mx) {
-    if (act_dtype != MOE_BF16 || (y_dtype != MOE_F32 && y_dtype != MOE_BF16)) return MOE_EUNSUPPORTED;
+    if (act_dtype != MOE_BF16 && !(act_dtype == MOE_MXFP8 && mx)) return MOE_EUNSUPPORTED;
+    if (y_dtype != MOE_F32 && y_dtype != MOE_BF16) return MOE_EUNSUPPORTED;
   } else {
     return MOE_EUNSUPPORTED;
   }
@@ -146,6 +150,7 @@ extern "C" int moe_expert_ffn(const void* x, int act_dtype, const int32_t* perm,
     MOE_LAUNCH_CHECK();
     return MOE_OK;
   }
+  if (act_dtype == MOE_MXFP8) return launch_ffn_mx8(p, T, y_dtype, stream, std::min(E, T * k));
   if (mx) {
     const bool gemm = path == MOE_PATH_GEMM ||
                       (path == MOE_PATH_AUTO && (long long)T * k > kMxGemmMinRowsPerExpert * E) ||

@@ -1,0 +1,62 @@
+// MXFP8 activations: rows of E4M3 codes with one E8M0 scale 2^(s - 127) per 32 elements (OCP
+// Microscaling Formats (MX) v1.0), in one buffer: codes [rows][d], then scales [rows][ss],
+// ss = d/32 rounded up to a multiple of 4 (so a row's scales of 128 elements are one aligned
+// word).
+//
+// Conversion of a block V (the MX rule, as for the MXFP4 weights): s = floor(log2 max |V|) - 8
+// + 127, at least 0 (8: the largest E4M3 exponent; 0 for an all-zero block); each element is
+// V / 2^(s - 127) rounded to nearest, ties to even, magnitudes beyond 448 saturating.  A block
+// that holds an infinity or a NaN has the scale 255 and codes 0x7F: every element is NaN.
+#pragma once
+
+#include "ffn_args.h"
+
+namespace moe {
+
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef short i16x2 __attribute__((ext_vector_type(2)));
+
+__host__ __device__ constexpr int mxfp8_scale_stride(int d) { return (d + 127) / 128 * 4; }
+
+__device__ __forceinline__ float e8m0_value(uint32_t s) {
+  return s ? __uint_as_float(s << 23) : __uint_as_float(0x00400000u);  // 2^(s - 127)
+}
+
+// Scale byte of a block whose largest |v| has the bits amax (an infinity or a NaN: 255).
+__device__ __forceinline__ uint32_t mxfp8_scale_of(uint32_t amax) {
+  const int e = (int)(amax >> 23);
+  return e == 255 ? 255u : (uint32_t)max(e - 8, 0);
+}
+
+// Four elements as E4M3 codes, element 0 in the low byte; sc = e8m0_value(s).  The conversion
+// instruction divides by the scale exactly and rounds to nearest even, but turns magnitudes
+// past 448 into NaN, so they are clamped first.
+__device__ __forceinline__ uint32_t mxfp8_pack4(float a, float b, float c, float d, uint32_t s,
+                                                float sc) {
+  if (s == 255u) return 0x7F7F7F7Fu;
+  const float m = 448.0f * sc;
+  i16x2 r = {0, 0};
+  r = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(r, __builtin_amdgcn_fmed3f(a, -m, m),
+                                               __builtin_amdgcn_fmed3f(b, -m, m), sc, false);
+  r = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(r, __builtin_amdgcn_fmed3f(c, -m, m),
+                                               __builtin_amdgcn_fmed3f(d, -m, m), sc, true);
+  return __builtin_bit_cast(uint32_t, r);
+}
+
+__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
+
+// Eight MFMA operand registers of an FP4 operand: the upper four are not read.
+__device__ __forceinline__ i32x8 fp4_operand(u32x4 c) {
+  return i32x8{(int)c[0], (int)c[1], (int)c[2], (int)c[3], 0, 0, 0, 0};
+}
+// An E4M3 operand: the lane's two 16-byte pieces.
+__device__ __forceinline__ i32x8 fp8_operand(u32x4 a, u32x4 b) {
+  return i32x8{(int)a[0], (int)a[1], (int)a[2], (int)a[3], (int)b[0], (int)b[1], (int)b[2], (int)b[3]};
+}
+
+// The expert FFN with MXFP8 activations and MXFP4 weights (arguments checked by moe_expert_ffn):
+// p.x holds T MXFP8 rows of d elements, p.h T * k of f.  `experts`: an upper bound on the
+// experts that the row filter admits.  Returns MOE_OK or MOE_EHIP.
+int launch_ffn_mx8(const FfnArgs& p, int T, int y_dtype, hipStream_t stream, int experts);
+
+}  // namespace moe

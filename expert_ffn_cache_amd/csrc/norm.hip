@@ -1,0 +1,343 @@
+// Residual addition and RMS norm of token rows, with the normalised rows in fp32 / bf16 and / or
+// MXFP8, and the MXFP8 conversions by themselves.
+//
+//   s = x + delta (rounded to x's type),  y = s * rsqrt(mean(s^2) + eps) * gamma
+//
+// delta is absent, a row of [T][d], or the token's gate-weighted sum of expert rows (the sum of
+// moe_combine, same order).  The row is held in registers between the two uses of s, so
+// every input is read once: HBM-bound for many rows, launch-bound for one.
+//
+// Work split: NT threads hold a row, a thread chunks of 8 consecutive elements (16 bytes of bf16,
+// two 16-byte loads of fp32), so four adjacent lanes hold an MXFP8 block and its largest
+// magnitude is found with two quad moves.  Up to 2048 elements a wave takes a row (no barrier;
+// four rows per workgroup), above that a workgroup of 256 or 1024 threads does.  Rows past
+// 1024 * 8 * kNormMaxChunks elements go through a loop that reads s back in a second pass.
+#include <algorithm>
+
+#include "mx8_dev.h"
+#include "wave.h"
+
+using namespace moe;
+
+namespace {
+
+enum { kDeltaNone = 0, kDeltaRow = 1, kDeltaCombine = 2 };
+constexpr int kNormMaxChunks = 4;
+
+struct NormArgs {
+  const void* x;
+  const void* delta;  // rows of delta, or the grouped expert rows
+  const int32_t* inv;
+  const float* w;
+  int k;
+  const void* gamma;
+  float eps;
+  int T, d;  // all rows
+  int t0, t1;  // rows of this launch
+  void* x_out;
+  void* y;
+  uint8_t* y8;
+  int x_dt, delta_dt, gamma_dt, y_dt;
+};
+
+struct F8 {
+  float v[8];
+};
+
+// Eight consecutive elements at element offset i (a multiple of 8) of a bf16 or fp32 array.
+__device__ __forceinline__ F8 load8(const void* p, size_t i, int dt) {
+  F8 r;
+  if (dt == MOE_F32) {
+    const f32x4 a = __builtin_bit_cast(f32x4, ldg16((const float*)p + i));
+    const f32x4 b = __builtin_bit_cast(f32x4, ldg16((const float*)p + i + 4));
+#pragma unroll
+    for (int q = 0; q < 4; ++q) { r.v[q] = a[q]; r.v[4 + q] = b[q]; }
+  } else {
+    const u32x4 a = ldg16((const uint16_t*)p + i);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      r.v[2 * q] = __uint_as_float(a[q] << 16);
+      r.v[2 * q + 1] = __uint_as_float(a[q] & 0xFFFF0000u);
+    }
+  }
+  return r;
+}
+
+__device__ __forceinline__ void store8(void* p, size_t i, int dt, const F8& s) {
+  if (dt == MOE_F32) {
+    *(f32x4*)((float*)p + i) = f32x4{s.v[0], s.v[1], s.v[2], s.v[3]};
+    *(f32x4*)((float*)p + i + 4) = f32x4{s.v[4], s.v[5], s.v[6], s.v[7]};
+  } else {
+    u32x4 o;
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      o[q] = (uint32_t)f32_to_bf16(s.v[2 * q]) | (uint32_t)f32_to_bf16(s.v[2 * q + 1]) << 16;
+    *(u32x4*)((uint16_t*)p + i) = o;
+  }
+}
+
+// The lane's 8 elements (column c of row t) of an MXFP8 row; the four lanes of a block are adjacent.
+__device__ __forceinline__ void store_mx8(uint8_t* y8, int T, int d, int t, int c, const F8& y) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int q = 0; q < 8; ++q) m = max(m, abs_bits(y.v[q]));
+  m = max(m, dpp_u32<0xB1>(m));  // quad_perm [1,0,3,2]
+  m = max(m, dpp_u32<0x4E>(m));  // quad_perm [2,3,0,1]
+  const uint32_t s = mxfp8_scale_of(m);
+  const float sc = e8m0_value(s);
+  *(u32x2*)(y8 + (size_t)t * d + c) = u32x2{mxfp8_pack4(y.v[0], y.v[1], y.v[2], y.v[3], s, sc),
+                                            mxfp8_pack4(y.v[4], y.v[5], y.v[6], y.v[7], s, sc)};
+  if ((c & 24) == 0) {
+    const int ss = mxfp8_scale_stride(d);
+    uint8_t* sr = y8 + (size_t)T * d + (size_t)t * ss;
+    sr[c >> 5] = (uint8_t)s;
+    if (c + 32 >= d)  // the padding of the row's scales
+      for (int b = d >> 5; b < ss; ++b) sr[b] = 0;
+  }
+}
+
+// s of one chunk: x + delta rounded to x's type.
+template <int DM>
+__device__ __forceinline__ F8 load_sum(const NormArgs& p, int t, int c) {
+  const size_t i = (size_t)t * p.d + c;
+  F8 s = load8(p.x, i, p.x_dt);
+  if (DM == kDeltaNone) return s;
+  F8 a;
+  if (DM == kDeltaRow) {
+    a = load8(p.delta, i, p.delta_dt);
+  } else {
+#pragma unroll
+    for (int q = 0; q < 8; ++q) a.v[q] = 0.f;
+    for (int j0 = 0; j0 < p.k; j0 += 8) {  // up to 8 rows' loads in flight, summed in ascending j
+      F8 r[8];
+      float w[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (j0 + j < p.k) {
+          r[j] = load8(p.delta, (size_t)p.inv[(size_t)t * p.k + j0 + j] * p.d + c, p.delta_dt);
+          w[j] = p.w[(size_t)t * p.k + j0 + j];
+        }
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (j0 + j < p.k) {
+#pragma unroll
+          for (int q = 0; q < 8; ++q) a.v[q] = fmaf(w[j], r[j].v[q], a.v[q]);
+        }
+    }
+  }
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    s.v[q] += a.v[q];
+    if (p.x_dt == MOE_BF16) s.v[q] = bf16_to_f32(f32_to_bf16(s.v[q]));
+  }
+  return s;
+}
+
+// Sum over the NT threads of a row (a wave or the whole workgroup), the same in each.
+template <int NT>
+__device__ __forceinline__ float row_sum(float v) {
+  v = wave_sum_f32(v);
+  if (NT == 64) return v;
+  __shared__ float part[NT / 64];
+  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
+  __syncthreads();
+  float r = 0.f;
+#pragma unroll
+  for (int i = 0; i < NT / 64; ++i) r += part[i];
+  return r;
+}
+
+__device__ __forceinline__ void norm_out(const NormArgs& p, int t, int c, const F8& s, float rstd) {
+  const F8 g = load8(p.gamma, c, p.gamma_dt);
+  F8 y;
+#pragma unroll
+  for (int q = 0; q < 8; ++q) y.v[q] = s.v[q] * rstd * g.v[q];
+  if (p.y) store8(p.y, (size_t)t * p.d + c, p.y_dt, y);
+  if (p.y8) store_mx8(p.y8, p.T, p.d, t, c, y);
+}
+
+__device__ __forceinline__ float row_rstd(float ss, int d, float eps) {
+  return 1.0f / sqrtf(ss / (float)d + eps);
+}
+
+template <int DM, int NT, int NCH>
+__global__ __launch_bounds__(NT < 256 ? 256 : NT) void rmsnorm_rows(NormArgs p) {
+  constexpr int RPB = NT < 256 ? 256 / NT : 1;
+  const int tid = NT < 256 ? threadIdx.x % NT : threadIdx.x;
+  const int t = p.t0 + (int)blockIdx.x * RPB + (NT < 256 ? (int)threadIdx.x / NT : 0);
+  if (t >= p.t1) return;  // whole waves (NT = 64), or never
+  F8 s[NCH];
+  float ss = 0.f;
+#pragma unroll
+  for (int i = 0; i < NCH; ++i) {
+    const int c = (tid + i * NT) * 8;
+    if (c < p.d) {
+      s[i] = load_sum<DM>(p, t, c);
+    } else {
+#pragma unroll
+      for (int q = 0; q < 8; ++q) s[i].v[q] = 0.f;
+    }
+#pragma unroll
+    for (int q = 0; q < 8; ++q) ss = fmaf(s[i].v[q], s[i].v[q], ss);
+  }
+  const float rstd = row_rstd(row_sum<NT>(ss), p.d, p.eps);
+#pragma unroll
+  for (int i = 0; i < NCH; ++i) {
+    const int c = (tid + i * NT) * 8;
+    if (c < p.d) {
+      if (p.x_out) store8(p.x_out, (size_t)t * p.d + c, p.x_dt, s[i]);
+      norm_out(p, t, c, s[i], rstd);
+    }
+  }
+}
+
+// Rows of any length: s is formed twice, or read back from x_out, which the same thread wrote.
+template <int DM>
+__global__ __launch_bounds__(1024) void rmsnorm_long(NormArgs p) {
+  const int t = p.t0 + (int)blockIdx.x;
+  float ss = 0.f;
+  for (int c = threadIdx.x * 8; c < p.d; c += 1024 * 8) {
+    const F8 s = load_sum<DM>(p, t, c);
+    if (p.x_out) store8(p.x_out, (size_t)t * p.d + c, p.x_dt, s);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) ss = fmaf(s.v[q], s.v[q], ss);
+  }
+  const float rstd = row_rstd(row_sum<1024>(ss), p.d, p.eps);
+  for (int c = threadIdx.x * 8; c < p.d; c += 1024 * 8) {
+    const F8 s = p.x_out ? load8(p.x_out, (size_t)t * p.d + c, p.x_dt) : load_sum<DM>(p, t, c);
+    norm_out(p, t, c, s, rstd);
+  }
+}
+
+// Rows of one launch: a launch's threads stay below 2^32.
+constexpr int kNormLaunchRows = 1 << 21;
+
+template <int DM>
+int launch_norm(NormArgs p, hipStream_t stream) {
+  const int d = p.d;
+  for (int t0 = 0; t0 < p.T; t0 += kNormLaunchRows) {
+    p.t0 = t0;
+    p.t1 = p.T - t0 < kNormLaunchRows ? p.T : t0 + kNormLaunchRows;
+    const dim3 rows(p.t1 - t0), quads((p.t1 - t0 + 3) / 4);
+    if (d <= 512) hipLaunchKernelGGL((rmsnorm_rows<DM, 64, 1>), quads, dim3(256), 0, stream, p);
+    else if (d <= 2048) hipLaunchKernelGGL((rmsnorm_rows<DM, 64, 4>), quads, dim3(256), 0, stream, p);
+    else if (d <= 4096) hipLaunchKernelGGL((rmsnorm_rows<DM, 256, 2>), rows, dim3(256), 0, stream, p);
+    else if (d <= 8192) hipLaunchKernelGGL((rmsnorm_rows<DM, 256, 4>), rows, dim3(256), 0, stream, p);
+    else if (d <= 1024 * 8 * kNormMaxChunks)
+      hipLaunchKernelGGL((rmsnorm_rows<DM, 1024, kNormMaxChunks>), rows, dim3(1024), 0, stream, p);
+    else hipLaunchKernelGGL((rmsnorm_long<DM>), rows, dim3(1024), 0, stream, p);
+    MOE_LAUNCH_CHECK();
+    if (p.t1 == p.T) break;  // t0 may not pass INT_MAX
+  }
+  return MOE_OK;
+}
+
+bool real_type(int dt) { return dt == MOE_F32 || dt == MOE_BF16; }
+
+// Checks shared by both norms: sizes and types, then (T > 0) pointers.
+int norm_check(const NormArgs& p) {
+  if (p.T < 0 || p.d <= 0 || p.d % 64 != 0) return MOE_EINVAL;
+  if (!(p.eps >= 0.f) || p.eps > 3e38f) return MOE_EINVAL;
+  if (!real_type(p.x_dt) || !real_type(p.gamma_dt) || (p.y && !real_type(p.y_dt))) return MOE_EUNSUPPORTED;
+  return MOE_OK;
+}
+int norm_pointers(const NormArgs& p) {
+  if (!p.x || !p.gamma || (!p.y && !p.y8)) return MOE_EINVAL;
+  for (const void* q : {p.x, p.delta, p.gamma, (const void*)p.x_out, (const void*)p.y, (const void*)p.y8})
+    if (!moe_aligned16(q)) return MOE_EINVAL;
+  return MOE_OK;
+}
+
+// ---- MXFP8 rows by themselves ----------------------------------------------------------
+__global__ __launch_bounds__(256) void mx8_quantize(const void* x, int x_dt, int T, int d,
+                                                    uint8_t* x8) {
+  const long n = (long)T * (d >> 3), step = (long)gridDim.x * 256;
+  for (long i = (long)blockIdx.x * 256 + threadIdx.x; i < n; i += step) {
+    const int t = (int)(i / (d >> 3)), c = (int)(i - (long)t * (d >> 3)) * 8;
+    store_mx8(x8, T, d, t, c, load8(x, (size_t)i * 8, x_dt));
+  }
+}
+
+// The 4 elements of an E4M3 code word times the block's scale (exact in fp32 and in bf16).
+__device__ __forceinline__ void mxfp8_unpack4(uint32_t w, float sc, float* v) {
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  const f32x2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(w, sc, false);
+  const f32x2 b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(w, sc, true);
+  v[0] = a[0]; v[1] = a[1]; v[2] = b[0]; v[3] = b[1];
+}
+
+__global__ __launch_bounds__(256) void mx8_dequantize(const uint8_t* x8, int T, int d, void* out,
+                                                      int out_dt) {
+  const int ss = mxfp8_scale_stride(d);
+  const long n = (long)T * (d >> 3), step = (long)gridDim.x * 256;
+  for (long i = (long)blockIdx.x * 256 + threadIdx.x; i < n; i += step) {
+    const int t = (int)(i / (d >> 3)), c = (int)(i - (long)t * (d >> 3)) * 8;
+    const u32x2 w = *(const u32x2*)(x8 + (size_t)i * 8);
+    const uint32_t s = ldg_u8(x8 + (size_t)T * d + (size_t)t * ss + (c >> 5));
+    const float sc = s == 255u ? __uint_as_float(0x7FC00000u) : e8m0_value(s);
+    F8 v;
+    mxfp8_unpack4(w[0], sc, v.v);
+    mxfp8_unpack4(w[1], sc, v.v + 4);
+    store8(out, (size_t)i * 8, out_dt, v);
+  }
+}
+
+unsigned chunk_grid(int T, int d) {
+  return (unsigned)std::min<long>(((long)T * (d >> 3) + 255) / 256, 1 << 20);
+}
+
+}  // namespace
+
+extern "C" size_t moe_mxfp8_bytes(int T, int d) {
+  if (T <= 0 || d <= 0 || d % 64 != 0) return 0;
+  return (size_t)T * ((size_t)d + mxfp8_scale_stride(d));
+}
+
+extern "C" int moe_mxfp8_quantize(const void* x, int x_dtype, int T, int d, void* x8,
+                                  hipStream_t stream) {
+  if (T < 0 || d <= 0 || d % 64 != 0) return MOE_EINVAL;
+  if (!real_type(x_dtype)) return MOE_EUNSUPPORTED;
+  if (T == 0) return MOE_OK;
+  if (!x || !x8 || !moe_aligned16(x) || !moe_aligned16(x8)) return MOE_EINVAL;
+  hipLaunchKernelGGL(mx8_quantize, dim3(chunk_grid(T, d)), dim3(256), 0, stream, x, x_dtype, T, d, (uint8_t*)x8);
+  MOE_LAUNCH_CHECK();
+  return MOE_OK;
+}
+
+extern "C" int moe_mxfp8_dequantize(const void* x8, int T, int d, void* x, int x_dtype,
+                                    hipStream_t stream) {
+  if (T < 0 || d <= 0 || d % 64 != 0) return MOE_EINVAL;
+  if (!real_type(x_dtype)) return MOE_EUNSUPPORTED;
+  if (T == 0) return MOE_OK;
+  if (!x || !x8 || !moe_aligned16(x) || !moe_aligned16(x8)) return MOE_EINVAL;
+  hipLaunchKernelGGL(mx8_dequantize, dim3(chunk_grid(T, d)), dim3(256), 0, stream, (const uint8_t*)x8, T, d, x, x_dtype);
+  MOE_LAUNCH_CHECK();
+  return MOE_OK;
+}
+
+extern "C" int moe_rmsnorm(const void* x, int x_dtype, const void* delta, int delta_dtype,
+                           const void* gamma, int gamma_dtype, float eps, int T, int d, void* x_out,
+                           void* y, int y_dtype, void* y8, hipStream_t stream) {
+  const NormArgs p{x, delta, nullptr, nullptr, 0, gamma, eps, T, d, 0, 0, x_out, y, (uint8_t*)y8,
+                   x_dtype, delta_dtype, gamma_dtype, y_dtype};
+  if (int rc = norm_check(p)) return rc;
+  if (delta && !real_type(delta_dtype)) return MOE_EUNSUPPORTED;
+  if (T == 0) return MOE_OK;
+  if (int rc = norm_pointers(p)) return rc;
+  return delta ? launch_norm<kDeltaRow>(p, stream) : launch_norm<kDeltaNone>(p, stream);
+}
+
+extern "C" int moe_combine_rmsnorm(const void* y_perm, int y_perm_dtype, const int32_t* inv,
+                                   const float* topk_w, int k, const void* x, int x_dtype,
+                                   const void* gamma, int gamma_dtype, float eps, int T, int d,
+                                   void* x_out, void* y, int y_dtype, void* y8, hipStream_t stream) {
+  const NormArgs p{x, y_perm, inv, topk_w, k, gamma, eps, T, d, 0, 0, x_out, y, (uint8_t*)y8,
+                   x_dtype, y_perm_dtype, gamma_dtype, y_dtype};
+  if (int rc = norm_check(p)) return rc;
+  if (k <= 0 || k > kMaxK || (long long)T * k >= (1ll << 31)) return MOE_EINVAL;
+  if (!real_type(y_perm_dtype)) return MOE_EUNSUPPORTED;
+  if (T == 0) return MOE_OK;
+  if (!y_perm || !inv || !topk_w) return MOE_EINVAL;
+  if (int rc = norm_pointers(p)) return rc;
+  return launch_norm<kDeltaCombine>(p, stream);
+}

@@ -8,9 +8,10 @@ buffers once and forwards pointers.
 """
 import torch
 
-from . import (MOE_F32, MOE_BF16, MOE_MXFP4, MOE_PATH_AUTO, moe_route, moe_permute, moe_route_permute,
+from . import (MOE_F32, MOE_BF16, MOE_MXFP4, MOE_MXFP8, MOE_PATH_AUTO, moe_route, moe_permute, moe_route_permute,
                moe_permute_workspace_bytes, moe_expert_ffn, moe_expert_ffn_workspace_bytes,
-               moe_combine, moe_decode_token, moe_decode_token_workspace_bytes)
+               moe_combine, moe_decode_token, moe_decode_token_workspace_bytes, moe_mxfp8_bytes,
+               moe_mxfp8_quantize, moe_rmsnorm, moe_combine_rmsnorm)
 
 
 def decode_token_supported(T, k, d, f, dtype, w_dtype, y_dtype):
@@ -30,10 +31,23 @@ def _tdtype(code):
     return torch.float32 if code == MOE_F32 else torch.bfloat16
 
 
+def _code(t):
+    """MOE_* code of a tensor's (or no tensor's) element type."""
+    if t is None:
+        return MOE_BF16
+    if t.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"fp32 or bf16 tensor expected, got {t.dtype}")
+    return MOE_F32 if t.dtype == torch.float32 else MOE_BF16
+
+
 class MoeLayer:
     def __init__(self, T, E, k, d, f, dtype=MOE_BF16, y_dtype=MOE_F32, device="cuda",
                  w_dtype=None):
-        """dtype: activations (and weights unless w_dtype is given, e.g. MOE_MXFP4)."""
+        """dtype: activations (and weights unless w_dtype is given, e.g. MOE_MXFP4).  With
+        MOE_MXFP8 activations (and MXFP4 weights, the default there) the layer keeps a buffer x8
+        of T MXFP8 rows, which norm() or quantize() fills."""
+        if w_dtype is None and dtype == MOE_MXFP8:
+            w_dtype = MOE_MXFP4
         self.T, self.E, self.k, self.d, self.f = T, E, k, d, f
         self.dtype, self.y_dtype = dtype, y_dtype
         self.w_dtype = dtype if w_dtype is None else w_dtype
@@ -53,6 +67,8 @@ class MoeLayer:
         self.ffn_ws = torch.empty(self.ffn_ws_bytes, dtype=torch.uint8, device=dev)
         self.y_perm = torch.empty((max(A, 1), d), dtype=_tdtype(y_dtype), device=dev)
         self.out = torch.empty((T, d), dtype=torch.float32, device=dev)
+        if dtype == MOE_MXFP8:
+            self.x8 = torch.empty(max(moe_mxfp8_bytes(T, d), 16), dtype=torch.uint8, device=dev)
         self.fusable = decode_token_supported(T, k, d, f, dtype, self.w_dtype, y_dtype)
         if self.fusable:
             # counters of the one-launch path: zero before the first call, zero after each
@@ -79,6 +95,23 @@ class MoeLayer:
                        key_base, self.ffn_ws, self.ffn_ws_bytes, self.y_perm, self.y_dtype, path,
                        self.status, stream)
 
+    def quantize(self, x, stream=None):
+        """x [T, d] (fp32 or bf16) into the layer's MXFP8 rows."""
+        moe_mxfp8_quantize(x, _code(x), self.T, self.d, self.x8, stream)
+        return self.x8
+
+    def norm(self, x, gamma, eps, delta=None, x_out=None, y=None, stream=None):
+        """Residual addition and RMS norm in front of the layer: x (+ delta) to x_out, the
+        normalised rows to y and, with MXFP8 activations, to the layer's MXFP8 rows."""
+        moe_rmsnorm(x, _code(x), delta, _code(delta), gamma, _code(gamma), eps, self.T, self.d, x_out,
+                    y, _code(y), self.x8 if self.dtype == MOE_MXFP8 else None, stream)
+
+    def combine_norm(self, x, gamma, eps, x_out=None, y=None, x8=None, stream=None):
+        """combine(), the residual addition and the next RMS norm in one launch (self.out is not
+        written): x + combined rows to x_out, the normalised rows to y and / or, in MXFP8, to x8."""
+        moe_combine_rmsnorm(self.y_perm, self.y_dtype, self.inv, self.w, self.k, x, _code(x), gamma,
+                            _code(gamma), eps, self.T, self.d, x_out, y, _code(y), x8, stream)
+
     def combine(self, stream=None):
         moe_combine(self.y_perm, self.y_dtype, self.inv, self.w, self.T, self.k, self.d,
                     self.out, stream)
@@ -95,7 +128,10 @@ class MoeLayer:
     def forward(self, x, logits, arena, entry_stride, expert_slot=None, path=MOE_PATH_AUTO,
                 stream=None, fused=None):
         """fused: None = the one-launch path where it applies (path AUTO), True = require it,
-        False = separate launches."""
+        False = separate launches.  With MXFP8 activations x is an MXFP8 buffer (uint8, e.g.
+        self.x8 after norm()) or fp32 / bf16 rows, which are quantised first."""
+        if self.dtype == MOE_MXFP8 and x.dtype != torch.uint8:
+            x = self.quantize(x, stream)
         if fused is None:
             fused = self.fusable and path == MOE_PATH_AUTO
         if fused:

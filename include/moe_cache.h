@@ -67,6 +67,7 @@ extern "C" {
 #define MOE_F32 0   /* IEEE binary32 */
 #define MOE_BF16 1  /* bfloat16 (upper half of binary32) */
 #define MOE_MXFP4 2 /* expert weights only: OCP MX FP4, see moe_entry_bytes */
+#define MOE_MXFP8 3 /* activation rows only: OCP MX FP8 (E4M3), see moe_mxfp8_bytes */
 
 /* Static text for a status code. */
 const char* moe_strerror(int status);
@@ -150,8 +151,56 @@ int moe_route_permute(const float* logits, int T, int E, int k, int32_t* topk_id
  * K/2*(r/16) + 64*(b/4) + 16*(b%4) + r%16. */
 size_t moe_entry_bytes(int d, int f, int w_dtype);
 
+/* Entries between the plain layout and MXFP4, for an arena or a host pool that is to hold
+ * MXFP4 experts and is given them in bf16 / fp32 (and back: to look at what the codes stand
+ * for, or to run an expert on the bf16 path).
+ * moe_entry_quantize: n entries of moe_entry_bytes(d, f, src_dtype) bytes each (MOE_F32 or
+ * MOE_BF16), src_stride bytes apart, to n MXFP4 entries dst_stride bytes apart.  Per block
+ * of 32 contraction elements V (OCP MX v1.0): scale 2^e, e = floor(log2 max|V|) - 2, at least
+ * -127 (an all-zero block: -127); each element V/2^e to the nearest E2M1 value, ties to the
+ * even code, magnitudes beyond 6 saturating to 6; the sign of a zero is kept.  A block that
+ * holds an infinity or a NaN gets the scale byte 255, which stands for NaN in every element.
+ * moe_entry_dequantize: the values (E2M1 value x scale, exact in both types but for bf16 /
+ * fp32 underflow below 2^-133 / 2^-149, which no scale reaches), scale byte 255 as NaN.
+ * Device memory, 16-byte aligned, as are the strides; strides at least the entry's bytes; src
+ * and dst must not overlap.  Bytes between entries are left as they are. */
+int moe_entry_quantize(const void* src, int src_dtype, size_t src_stride, int n, int d, int f,
+                       void* dst, size_t dst_stride, hipStream_t stream);
+int moe_entry_dequantize(const void* src, size_t src_stride, int n, int d, int f, void* dst,
+                         int dst_dtype, size_t dst_stride, hipStream_t stream);
+
+/* Activation rows in MXFP8 (OCP MX v1.0: E4M3 elements, one E8M0 scale 2^(s - 127) per 32
+ * consecutive elements of a row), in one buffer of moe_mxfp8_bytes(T, d) bytes:
+ *   [codes: T rows of d bytes][scales: T rows of ss bytes, ss = d/32 rounded up to a multiple
+ *   of 4]
+ * (a row's scale bytes past d/32 are written as 0 and never used).  0 for T <= 0 or d not a
+ * positive multiple of 64. */
+size_t moe_mxfp8_bytes(int T, int d);
+
+/* Rows x [T][d] in x_dtype (MOE_F32 or MOE_BF16) to MXFP8 and back.  Per block V: s =
+ * floor(log2 max|V|) - 8 + 127, at least 0 (also for an all-zero block); each element
+ * V/2^(s-127) to the nearest E4M3 value, ties to even, magnitudes beyond 448 saturating to
+ * 448; a block that holds an infinity or a NaN gets scale 255 and codes 0x7F and stands for
+ * NaN in every element.  Back: code value x scale (rounded only where bf16 underflows). */
+int moe_mxfp8_quantize(const void* x, int x_dtype, int T, int d, void* x8, hipStream_t stream);
+int moe_mxfp8_dequantize(const void* x8, int T, int d, void* x, int x_dtype, hipStream_t stream);
+
+/* Residual addition and RMS norm, the step in front of the router and the experts:
+ *   s = x + delta, rounded to x_dtype (s = x where delta is NULL)
+ *   y = s / sqrt(mean(s^2) + eps) * gamma      (fp32 arithmetic, rounded once)
+ * x [T][d] in x_dtype, delta [T][d] in delta_dtype (e.g. the fp32 rows of moe_combine),
+ * gamma [d] in gamma_dtype, each MOE_F32 or MOE_BF16.  Writes x_out [T][d] = s in x_dtype (NULL:
+ * not wanted), y [T][d] in y_dtype (NULL: not wanted) and y8, the rows of y before their
+ * rounding to y_dtype in MXFP8 as by moe_mxfp8_quantize (NULL: not wanted); y or y8 must be
+ * given.  x_out may be x itself, or delta where the types are the same; y and y8 may not overlap
+ * an input.  eps >= 0 and finite; a row of zeros with eps = 0 gives NaN, as the formula does.
+ * Deterministic; rows do not affect one another. */
+int moe_rmsnorm(const void* x, int x_dtype, const void* delta, int delta_dtype, const void* gamma,
+                int gamma_dtype, float eps, int T, int d, void* x_out, void* y, int y_dtype,
+                void* y8, hipStream_t stream);
+
 /* Workspace bytes for moe_expert_ffn: the SwiGLU intermediate [T*k][f] (2 bytes per unit,
- * 4 with MOE_F32 activations), and up to 16 tokens with MOE_BF16 activations 4 bytes per
+ * 4 with MOE_F32 activations; with MOE_MXFP8 activations T*k MXFP8 rows of f units), and up to 16 tokens with MOE_BF16 activations 4 bytes per
  * unit, room for the one-launch MXFP4 path (see moe_expert_ffn's ws). */
 size_t moe_expert_ffn_workspace_bytes(int T, int k, int f, int act_dtype);
 
@@ -173,7 +222,11 @@ size_t moe_expert_ffn_workspace_bytes(int T, int k, int f, int act_dtype);
  *  end); MOE_BF16 weights need MOE_BF16 activations, y fp32 or bf16, and
  *  round h to bf16 before the down projection.  MOE_MXFP4 weights (entry
  *  layout under moe_entry_bytes) need MOE_BF16 activations; each weight is its
- *  exact value (E2M1 value x block scale), the rest as for MOE_BF16.  MXFP4 runs
+ *  exact value (E2M1 value x block scale), the rest as for MOE_BF16.  With MOE_MXFP4
+ *  weights the activations may also be MOE_MXFP8: x is then an MXFP8 buffer of T rows (see
+ *  moe_mxfp8_bytes), y fp32 or bf16; the products take the codes and scales of both sides as
+ *  they are (block-scaled matrix instructions, fp32 accumulation), and h is rounded to MXFP8
+ *  (as by moe_mxfp8_quantize) before the down projection.  MXFP4 with MOE_BF16 runs
  *  on both paths (the weight-streaming one for d, f <= 8128).  With MOE_BF16
  *  weights the GEMM path needs T*d, T*k*f and 3*d*f each <= 2^32 (it keeps
  *  element offsets in 32 bits): MOE_PATH_GEMM past that returns
@@ -181,8 +234,8 @@ size_t moe_expert_ffn_workspace_bytes(int T, int k, int f, int act_dtype);
  *  slot_key (nullable, device, [S]): when given, a slot whose key is not
  *  key_base + e, or a negative slot, sets *status = MOE_ERANGE and that
  *  expert's rows are not written (stale-cache detection).
- *  ws: 16-byte aligned, at least T*k*f*2 bytes (4 with MOE_F32 activations), or
- *  MOE_EINVAL.  With MOE_MXFP4 weights on the weight-streaming path, T <= 16,
+ *  ws: 16-byte aligned, at least T*k*f*2 bytes (4 with MOE_F32 activations,
+ *  moe_mxfp8_bytes(T*k, f) with MOE_MXFP8), or MOE_EINVAL.  With MOE_MXFP4 weights and MOE_BF16 activations on the weight-streaming path, T <= 16,
  *  min(E, T*k)*f >= 65536 and at least T*k*f*4 bytes (what
  *  moe_expert_ffn_workspace_bytes returns there), both projections run in one launch that
  *  exchanges h through tagged entries in ws (zeroed by a small kernel first); the results
@@ -203,7 +256,7 @@ int moe_expert_ffn(const void* x, int act_dtype, const int32_t* perm, const int3
  * up that device's array address once).  Every other argument, result and error is as for
  * moe_expert_ffn, which it calls with the array as ws (so calls of up to 16 tokens whose
  * tagged entries fit take the one-launch MXFP4 path).  A call whose intermediate (T*k*f*2
- * bytes, 4 with MOE_F32 activations) exceeds the array returns MOE_ETOOBIG before anything
+ * bytes, 4 with MOE_F32 activations, T*k MXFP8 rows with MOE_MXFP8) exceeds the array returns MOE_ETOOBIG before anything
  * is enqueued.  All calls on
  * one GPU share its array and each overwrites it: calls that may overlap in time on one GPU
  * (different streams, or different host threads) race and give undefined results; order them
@@ -228,6 +281,16 @@ size_t moe_expert_ffn_noalloc_max_bytes(void);
  * experts), with the gate weights of moe_route. */
 int moe_combine(const void* y_perm, int y_dtype, const int32_t* inv, const float* topk_w, int T,
                 int k, int d, float* out, hipStream_t stream);
+
+/* moe_combine, the residual addition and the next RMS norm in one launch: moe_rmsnorm with
+ * delta = sum_j topk_w[t][j] * y_perm[inv[t*k+j]][:] (the sum of moe_combine, fp32, same
+ * order), which is not written anywhere.  Bit-identical to moe_combine followed by moe_rmsnorm
+ * with its fp32 rows as delta.  y_perm, inv, topk_w, k as for moe_combine, the rest as for
+ * moe_rmsnorm; x_out may be x itself. */
+int moe_combine_rmsnorm(const void* y_perm, int y_perm_dtype, const int32_t* inv,
+                        const float* topk_w, int k, const void* x, int x_dtype, const void* gamma,
+                        int gamma_dtype, float eps, int T, int d, void* x_out, void* y, int y_dtype,
+                        void* y8, hipStream_t stream);
 
 /* Workspace bytes moe_decode_token needs: a 256-byte header (the launch epoch
  * word), then the SwiGLU intermediate as 8-byte entries (up to two bf16 values

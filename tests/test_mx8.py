@@ -1,0 +1,154 @@
+"""MXFP8 operators without a GPU: pins of the float64 definitions (hand-computed blocks, brute
+force) and the argument checks of the entry points, which return before anything is enqueued."""
+import numpy as np
+import pytest
+
+import expert_ffn_cache_amd as moe
+from oracle import mx8
+
+
+# ---------------------------------------------------------------- the definitions
+def test_e4m3_codes_from_their_fields():
+    for c in range(127):
+        e, m = c >> 3, c & 7
+        assert mx8.E4M3[c] == (m * 2.0 ** -9 if e == 0 else (8 + m) * 2.0 ** (e - 10))
+    assert mx8.E4M3[126] == 448.0 and np.all(np.diff(mx8.E4M3) > 0)
+
+
+def test_hand_quantised_block():
+    """max |v| = 500 * 2^-5: floor(log2) = 3, scale 2^(3 - 8) = 2^-5.  Scaled values by hand:
+    500 saturates to 448; 17 ties between 16 and 18 and goes to 16 (even), 19 to 20; 2^-10 ties
+    between 0 and 2^-9 and goes to 0; 1.5 * 2^-9 ties to 2^-8; -0.3 rounds to -0.3125."""
+    scaled = [500, 17, 19, 2.0 ** -10, 1.5 * 2.0 ** -9, -0.3, 2.0 ** -9, -448]
+    want = [448, 16, 20, 0, 2.0 ** -8, -0.3125, 2.0 ** -9, -448]
+    v = np.zeros((1, 32))
+    v[0, :8] = np.array(scaled) * 2.0 ** -5
+    c, s = mx8.quantize(v)
+    assert s[0, 0] == 127 - 5
+    np.testing.assert_array_equal(mx8.dequantize(c, s)[0, :8], np.array(want) * 2.0 ** -5)
+
+
+def test_random_blocks_round_to_a_nearest_value():
+    r = np.random.default_rng(3)
+    for _ in range(200):
+        v = r.standard_normal((1, 32)) * r.choice([1e-30, 1e-3, 1.0, 1e20])
+        c, s = mx8.quantize(v)
+        X = 2.0 ** (int(s[0, 0]) - 127)
+        assert 256 <= np.abs(v).max() / X < 512
+        q = mx8.dequantize(c, s)[0]
+        for a, b in zip(v[0], q):
+            dist = np.abs(mx8.E4M3 - min(abs(a) / X, 448.0))
+            assert abs(abs(b) / X - min(abs(a) / X, 448.0)) == dist.min()
+
+
+@pytest.mark.parametrize("v,scale", [(0.0, 0), (2.0 ** -126, 0), (2.0 ** -119, 0), (2.0 ** -118, 1),
+                                     (2.0 ** -140, 0), (3e38, 246), (np.inf, 255), (np.nan, 255)])
+def test_scale_bytes(v, scale):
+    b = np.zeros((1, 32))
+    b[0, 7] = v
+    c, s = mx8.quantize(b)
+    assert s[0, 0] == scale
+    if scale == 255:
+        assert np.all(c == 0x7F) and np.isnan(mx8.dequantize(c, s)).all()
+
+
+def test_span_holds_what_nearby_numbers_round_to():
+    r = np.random.default_rng(4)
+    v = r.standard_normal((50, 64))
+    v[0, 0] = 4.0  # a block whose largest magnitude is a power of two: its scale may be either
+    v[0, 1:32] = np.clip(v[0, 1:32], -3.9, 3.9)
+    err = 1e-3 * np.abs(v)
+    lo, hi = mx8.span(v, err)
+    for _ in range(20):
+        q = mx8.dequantize(*mx8.quantize(v + err * r.uniform(-1, 1, v.shape)))
+        assert np.all(q >= lo) and np.all(q <= hi)
+    assert np.mean(hi > lo) < 0.2
+
+
+# ---------------------------------------------------------------- refusals
+F32, BF16, X4, X8 = moe.MOE_F32, moe.MOE_BF16, moe.MOE_MXFP4, moe.MOE_MXFP8
+A = 1 << 20  # an aligned stand-in address: nothing is dereferenced on these paths
+EINVAL, EUNSUP = moe.MOE_EINVAL, moe.MOE_EUNSUPPORTED
+
+
+def test_mxfp8_sizes():
+    assert moe.moe_mxfp8_bytes(8, 4096) == 8 * (4096 + 128)
+    assert moe.moe_mxfp8_bytes(3, 64) == 3 * (64 + 4)      # 2 scales, filled up to 4 bytes
+    assert moe.moe_mxfp8_bytes(3, 320) == 3 * (320 + 12)   # 10 scales, filled up to 12
+    assert moe.moe_mxfp8_bytes(1 << 20, 8192) == (1 << 20) * (8192 + 256)
+    for T, d in ((0, 64), (-1, 64), (1, 0), (1, 100), (1, -64)):
+        assert moe.moe_mxfp8_bytes(T, d) == 0
+    nws = moe.moe_expert_ffn_workspace_bytes(333, 8, 768, X8)
+    assert nws >= moe.moe_mxfp8_bytes(333 * 8, 768) and nws % 256 == 0
+
+
+@pytest.mark.parametrize("change,want", [
+    (dict(x=None), EINVAL), (dict(x8=None), EINVAL), (dict(x=A + 4), EINVAL), (dict(x8=A + 8), EINVAL),
+    (dict(dt=X4), EUNSUP), (dict(dt=X8), EUNSUP), (dict(dt=9), EUNSUP), (dict(T=-1), EINVAL),
+    (dict(d=0), EINVAL), (dict(d=96), EINVAL), (dict(d=-64), EINVAL), (dict(T=0, x=None), 0)])
+def test_conversions_refuse(change, want):
+    a = dict(dict(x=A, dt=F32, T=4, d=128, x8=A), **change)
+    L = moe.lib()
+    assert L.moe_mxfp8_quantize(a["x"], a["dt"], a["T"], a["d"], a["x8"], None) == want
+    assert L.moe_mxfp8_dequantize(a["x8"], a["T"], a["d"], a["x"], a["dt"], None) == want
+
+
+@pytest.mark.parametrize("change,want", [
+    (dict(x=None), EINVAL), (dict(gamma=None), EINVAL), (dict(y=None, y8=None), EINVAL),
+    (dict(x=A + 2), EINVAL), (dict(delta=A + 4), EINVAL), (dict(gamma=A + 8), EINVAL),
+    (dict(out=A + 4), EINVAL), (dict(y=A + 4), EINVAL), (dict(y8=A + 1), EINVAL),
+    (dict(xdt=X8), EUNSUP), (dict(ddt=X4), EUNSUP), (dict(gdt=7), EUNSUP), (dict(ydt=X8), EUNSUP),
+    (dict(eps=-1e-6), EINVAL), (dict(eps=float("nan")), EINVAL), (dict(eps=float("inf")), EINVAL),
+    (dict(T=-1), EINVAL), (dict(d=100), EINVAL), (dict(d=0), EINVAL), (dict(T=0, x=None), 0)])
+def test_rmsnorm_refuses(change, want):
+    a = dict(dict(x=A, xdt=BF16, delta=A, ddt=F32, gamma=A, gdt=BF16, eps=1e-6, T=4, d=128, out=A, y=A,
+                  ydt=BF16, y8=A), **change)
+    L = moe.lib()
+    tail = (a["x"], a["xdt"], a["gamma"], a["gdt"], a["eps"], a["T"], a["d"], a["out"], a["y"], a["ydt"], a["y8"], None)
+    assert L.moe_rmsnorm(a["x"], a["xdt"], a["delta"], a["ddt"], *tail[2:]) == want
+    assert L.moe_combine_rmsnorm(a["delta"], a["ddt"], A, A, 2, *tail) == want
+
+
+def test_combine_rmsnorm_refuses_its_own():
+    tail = (A, BF16, A, BF16, 1e-6, 4, 128, A, A, BF16, A, None)
+    L = moe.lib()
+    for head, want in (((None, F32, A, A, 2), EINVAL), ((A, F32, None, A, 2), EINVAL), ((A, F32, A, None, 2), EINVAL),
+                       ((A, F32, A, A, 0), EINVAL), ((A, F32, A, A, 17), EINVAL), ((A, X8, A, A, 2), EUNSUP)):
+        assert L.moe_combine_rmsnorm(*head, *tail) == want
+
+
+@pytest.mark.parametrize("change,want", [
+    (dict(plain=None), EINVAL), (dict(mx=None), EINVAL), (dict(plain=A + 8), EINVAL), (dict(mx=A + 4), EINVAL),
+    (dict(dt=X4), EUNSUP), (dict(n=-1), EINVAL), (dict(d=100), EINVAL), (dict(f=0), EINVAL),
+    (dict(ps=3 * 128 * 64 * 2 - 16), EINVAL), (dict(ps=3 * 128 * 64 * 2 + 8), EINVAL),
+    (dict(ms=3 * 128 * 64 * 17 // 32 - 16), EINVAL), (dict(ms=3 * 128 * 64 * 17 // 32 + 4), EINVAL),
+    (dict(d=1 << 20, f=1 << 20, ps=1 << 50, ms=1 << 50), EINVAL),  # block numbers past 32 bits
+    (dict(n=0, plain=None), 0)])
+def test_entry_conversions_refuse(change, want):
+    a = dict(dict(plain=A, dt=BF16, ps=3 * 128 * 64 * 2, n=1, d=128, f=64, mx=A, ms=3 * 128 * 64 * 17 // 32), **change)
+    L = moe.lib()
+    assert L.moe_entry_quantize(a["plain"], a["dt"], a["ps"], a["n"], a["d"], a["f"], a["mx"], a["ms"], None) == want
+    assert L.moe_entry_dequantize(a["mx"], a["ms"], a["n"], a["d"], a["f"], a["plain"], a["dt"], a["ps"], None) == want
+
+
+def test_expert_ffn_with_mxfp8_activations_refuses():
+    eb = moe.moe_entry_bytes(4096, 2048, X4)
+    base = [A, X8, A, A, 8, 6, 256, 4096, 2048, None, A, eb, X4, None, None, 0, A,
+            moe.moe_mxfp8_bytes(48, 2048), A, F32, 0, None, None]
+
+    def rc(**kw):
+        a = list(base)
+        for i, v in kw.items():
+            a[int(i[1:])] = v
+        return moe.lib().moe_expert_ffn(*a)
+    assert rc(_12=BF16, _11=3 * 4096 * 2048 * 2) == EUNSUP  # MXFP4 weights only
+    assert rc(_12=F32, _11=3 * 4096 * 2048 * 4) == EUNSUP
+    assert rc(_19=X8) == EUNSUP and rc(_19=X4) == EUNSUP     # y in fp32 or bf16
+    assert rc(_17=base[17] - 1) == EINVAL                    # workspace below T*k MXFP8 rows
+    assert rc(_11=eb - 16) == EINVAL and rc(_7=4000) == EINVAL and rc(_0=None) == EINVAL
+    assert rc(_0=A + 8) == EINVAL and rc(_20=3) == EINVAL
+    assert rc(_4=0) == 0
+    # the no-allocation form: T*k*(f + scales) beyond its array
+    T = moe.moe_expert_ffn_noalloc_max_bytes() // (2048 + 64) + 1
+    na = [A, X8, A, A, T, 1, 256, 4096, 2048, None, A, eb, X4, None, None, 0, A, F32, 0, None, None]
+    assert moe.lib().moe_expert_ffn_noalloc(*na) == moe.MOE_ETOOBIG
