@@ -42,6 +42,7 @@ constexpr int kMxMaxRows = 16;
 // (T*k / E), MXFP4 experts above kMxGemmMinRowsPerExpert (their streaming path, with the row
 // split above, stays ahead to about 5 rows per expert at Zipf 0.2 and beyond 8 when skewed).
 constexpr long long kGemmMinRowsPerExpert = 2, kMxGemmMinRowsPerExpert = 8;
+constexpr long long kMx8GemmMinRowsPerExpert = 4;
 // Rounds of resident workgroups in the row-split dot-product launches (each loops over items).
 constexpr int kDotSplitRounds = 2;
 
@@ -133,6 +134,8 @@ extern "C" int moe_expert_ffn(const void* x, int act_dtype, const int32_t* perm,
   }
   const bool bf16_gemm_fits = ffn_gemm_supported(T, k, d, f);
   if (w_dtype == MOE_BF16 && path == MOE_PATH_GEMM && !bf16_gemm_fits) return MOE_EUNSUPPORTED;
+  const bool mx8_gemm_fits = ffn_mx8_gemm_supported(T, k, d, f);
+  if (act_dtype == MOE_MXFP8 && path == MOE_PATH_GEMM && !mx8_gemm_fits) return MOE_EUNSUPPORTED;
   const size_t need = mx ? moe_entry_bytes(d, f, w_dtype) : 3 * (size_t)d * f * (f32 ? 4 : 2);
   if (entry_stride < need || entry_stride % 16 != 0) return MOE_EINVAL;
   if (T == 0) return MOE_OK;
@@ -150,7 +153,12 @@ extern "C" int moe_expert_ffn(const void* x, int act_dtype, const int32_t* perm,
     MOE_LAUNCH_CHECK();
     return MOE_OK;
   }
-  if (act_dtype == MOE_MXFP8) return launch_ffn_mx8(p, T, y_dtype, stream, std::min(E, T * k));
+  if (act_dtype == MOE_MXFP8) {
+    if (path == MOE_PATH_AUTO)
+      path = (long long)T * k <= kMx8GemmMinRowsPerExpert * E || !mx8_gemm_fits ? MOE_PATH_GEMV : MOE_PATH_GEMM;
+    if (path == MOE_PATH_GEMM) return launch_ffn_mx8_gemm(p, T, y_dtype, stream);
+    return launch_ffn_mx8(p, T, y_dtype, stream, std::min(E, T * k));
+  }
   if (mx) {
     const bool gemm = path == MOE_PATH_GEMM ||
                       (path == MOE_PATH_AUTO && (long long)T * k > kMxGemmMinRowsPerExpert * E) ||
