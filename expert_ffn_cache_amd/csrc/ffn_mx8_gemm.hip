@@ -1,0 +1,412 @@
+// Expert FFN with MXFP8 activations and MXFP4 weights for many rows per expert: a grouped GEMM on
+// v_mfma_scale_f32_32x32x64_f8f6f4, codes and scales of both sides as they are stored.
+//
+// Tile: 256 weight rows x 128 token rows of one expert, 4 waves, two workgroups a CU; a wave
+// computes 64 weight rows x up to 128 token rows (2 x 4 accumulator tiles).  A = weights, B = tokens, so a lane holds
+// 16 of the 32 weight rows of one token (the other 16 are in the lane 32 away): in gate/up
+// (tile 0 gate, tile 1 up of the same 32 units) a block of h is two lanes, and its MXFP8 scale
+// takes one exchange.
+//
+// k steps of 128 elements (one tile column of the entry layout) go through an LDS ring by direct
+// global-to-LDS loads.  Operand order of the instruction (lane 32 g + i, elements of the 64 in
+// step half kh): FP4 row i: elements 32 g .. 32 g + 31, which is block 2 kh + g of the row and one
+// 16-byte slot of the weight tile; E4M3 row i: 16 g .. and 32 + 16 g .., two 16-byte pieces; the
+// scale of lane 32 g + i is that of row i, block 2 kh + g.  A token row's four scales of the step
+// are one word, shifted so that the lane's two are bytes 0 and 2, which the instruction
+// selects.  Token rows lie at 128 bytes with their 16-byte pieces permuted by (row / 2) mod 8
+// (16 lanes that read one piece of 16 rows then touch all banks once).
+//
+// Work list: persistent workgroups over (expert, weight tile, token tile), derived from the
+// offsets on the device; consecutive items, which share weights or token rows, go to one XCD.
+// Token tiles go four at a time to a weight tile, so its codes come from L2 for three of them.
+#include <algorithm>
+#include <type_traits>
+
+#include "mx8_dev.h"
+
+namespace moe {
+namespace {
+
+constexpr int kGCodes = 16 * 1024;       // codes of a stage: strip s at s * 1024, slot 16 q + i
+constexpr int kGScales = 16 * 64;        // weight scales of a stage: strip s at s * 64
+
+constexpr int kGM = 128;                 // token rows of a tile
+// A stage: weight scales, token rows (row r at r * 128), codes.
+constexpr int kGTokAt = kGScales;
+constexpr int kGCodeAt = kGTokAt + kGM * 128;
+constexpr int kGStage = kGCodeAt + kGCodes;
+// Token scales come in chunks of 8 steps, two of them in LDS: row r's word of step n of a chunk at
+// word r * 8 + (n ^ (r / 8) mod 8).  One load brings 8 rows x 32 bytes; a word per row and step
+// instead would fetch a whole cache line for it (that alone cost half of the time).
+constexpr int kGTsWords = kGM * 8;
+
+__device__ __forceinline__ uint32_t g_lds_addr(const void* p) {
+  return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)p;
+}
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+// 64 lanes x 16 (4) bytes from base + the lane's offset to consecutive LDS bytes from `lds` on.
+__device__ __forceinline__ void g_load16(const void* base, uint32_t off, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base) : "memory", "m0");
+}
+__device__ __forceinline__ void g_load4(const void* base, uint32_t off, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dword %1, %2" ::"s"(lds), "v"(off), "s"(base) : "memory", "m0");
+}
+#pragma clang diagnostic pop
+template <int N>
+__device__ __forceinline__ void g_wait_loads() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(waitcnt_imm(N, 7, 15));
+  asm volatile("" ::: "memory");
+}
+
+// SiLU(g) * u with the hardware reciprocal (1 ulp), as in the bf16 GEMMs.
+__device__ __forceinline__ float g_swiglu(float g, float u) {
+  return g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)) * u;
+}
+
+// Words w[0..3] of lane 32 g + i are elements 8 j + 4 g .. of row i's 32 (4 bytes each or packed
+// wider); afterwards lane 32 g + i holds words of elements 16 g .. 16 g + 15 in order.
+__device__ __forceinline__ void g_pair_rows(uint32_t (&w)[4]) {
+  const auto a = __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false);
+  const auto b = __builtin_amdgcn_permlane32_swap(w[1], w[3], false, false);
+  w[0] = a[0]; w[1] = a[1]; w[2] = b[0]; w[3] = b[1];
+}
+
+template <int MODE, int YDT>  // MODE 0: gate/up (h out), 1: down (y out)
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2)))
+void m8_tile(FfnArgs p, const uint8_t* ascales, uint32_t last_piece, uint8_t* hscales, int n_ntiles) {
+  __shared__ __attribute__((aligned(1024))) uint8_t sm[2][kGStage];
+  __shared__ int s_pref[kMaxE + 1];
+  __shared__ int s_part[4];
+  __shared__ __attribute__((aligned(256))) uint32_t s_ts[2][kGTsWords];
+  __shared__ uint32_t s_row[kGM];  // where the tile's token rows' scales start
+
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  {  // token tiles per expert and their prefix (E <= 1024: 4 experts per thread)
+    constexpr int PT = kMaxE / 256;
+    int c[PT], tot = 0;
+#pragma unroll
+    for (int q = 0; q < PT; ++q) {
+      const int e = tid * PT + q;
+      c[q] = e < p.E && active(p, e) ? (p.offsets[e + 1] - p.offsets[e] + kGM - 1) / kGM : 0;
+      tot += c[q];
+    }
+    int x = tot;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+      const int y = __shfl_up(x, off);
+      if (lane >= off) x += y;
+    }
+    if (lane == 63) s_part[wave] = x;
+    __syncthreads();
+    int run = x - tot;
+#pragma unroll
+    for (int w = 0; w < 4; ++w)
+      if (w < wave) run += s_part[w];
+#pragma unroll
+    for (int q = 0; q < PT; ++q) {
+      const int e = tid * PT + q;
+      if (e < p.E) s_pref[e] = run;
+      run += c[q];
+      if (e == p.E - 1) s_pref[p.E] = run;
+    }
+    __syncthreads();
+  }
+  const int total_items = s_pref[p.E] * n_ntiles;
+  const int K = MODE == 0 ? p.d : p.f, R = MODE == 0 ? p.f : p.d;
+  const int nk = (K + 127) >> 7, ss = mxfp8_scale_stride(K);
+  const bool half = (K & 127) != 0;  // the last step holds 64 elements
+  const size_t fd = (size_t)p.f * p.d;
+  const int ng = gridDim.x, per_xcd = ng >> 3;
+  const int pos = (blockIdx.x & 7) * per_xcd + (blockIdx.x >> 3);
+  const uint8_t* acodes = (const uint8_t*)(MODE == 0 ? p.x : p.h);
+
+  for (int j = pos; j < total_items; j += ng) {
+    const int q = j / n_ntiles;
+    int lo = 0, hi = p.E;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (s_pref[mid] <= q) lo = mid; else hi = mid - 1;
+    }
+    const int e = lo;
+    const int m_e = s_pref[e + 1] - s_pref[e];
+    const int local = j - s_pref[e] * n_ntiles;
+    const int grp = local / (4 * n_ntiles), first_m = grp * 4;
+    const int gsz = min(4, m_e - first_m), in = local - grp * 4 * n_ntiles;
+    const int nt = in / gsz, mt = first_m + (in - nt * gsz);
+    const uint8_t* W = (const uint8_t*)entry_of(p, e);
+    if (!W) continue;
+    const int n0 = p.offsets[e] + mt * kGM;
+    const int rows = min(kGM, p.offsets[e + 1] - n0);
+    const int mtiles = (rows + 31) >> 5;
+
+    // this lane's sources: token rows (4 wave + t) * 8 + lane / 8, piece (lane & 7) unpermuted
+    uint32_t oa[4];
+    int ln = lane;
+    asm volatile("" : "+v"(ln));  // keeps lane addresses out of the loop's live registers
+    const int g = ln >> 5, i32 = ln & 31;
+    auto row_at = [&](int r) { return (uint32_t)(MODE == 0 ? p.perm[n0 + r] / p.k : n0 + r); };
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+      oa[t] = row_at(min((4 * wave + t) * 8 + (ln >> 3), rows - 1)) * (uint32_t)K +
+              ((ln & 7) ^ ((((4 * wave + t) * 8 + (ln >> 3)) >> 1) & 7)) * 16;
+    // strip s of the tile: 16 weight rows (past the matrix: row 0, its results dropped)
+    auto strip = [&](int s, size_t& co, size_t& so) {
+      int r0, m = 2;
+      if (MODE == 0) {
+        m = (s >> 1) & 1;
+        r0 = nt * 128 + (s >> 2) * 32 + (s & 1) * 16;
+      } else {
+        r0 = nt * 256 + s * 16;
+      }
+      if (r0 >= R) r0 = 0;
+      co = (size_t)m * (fd / 2) + (size_t)r0 * (K / 2);
+      so = 3 * (fd / 2) + (size_t)m * (fd / 32) + (size_t)r0 * (K / 32);
+    };
+    // A wave loads 32 token rows, the codes and the scales of its own four strips, and an eighth of
+    // a quarter of the next token scale chunk (a pair of waves the same): no branch, the same
+    // ten loads in each.  In a last step of 64 elements the second half of a code tile and of its scales does
+    // not exist (the first is read twice); the pieces of token rows past their end are other
+    // rows' or, at the buffer's last row, its last bytes.  None of that is used.
+    const uint8_t* cp[4];
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      size_t co, so;
+      strip(wave * 4 + s, co, so);
+      cp[s] = W + co;
+    }
+    const uint8_t* const wsp = W + 3 * (fd / 2);
+    uint32_t ows;
+    {
+      size_t co, so;
+      strip(wave * 4 + (ln >> 4), co, so);
+      ows = (uint32_t)(so - 3 * (fd / 2)) + (ln & 15) * 4;
+    }
+    // Load i of 16 of token scale chunk c: rows 8 i .. 8 i + 7 (words past a row's end: its last).
+    auto ts_row = [&](int i) { return s_row[i * 8 + (ln >> 3)]; };
+    auto issue_ts = [&](int c, int i, uint32_t row) {
+      const int n = min(c * 8 + ((ln & 7) ^ (i & 7)), (ss >> 2) - 1);
+      g_load4(ascales, row + 4 * n, g_lds_addr(s_ts[c & 1]) + i * 256);
+    };
+    // Stage S <- step kt (at most nk - 1), and load 2 (kt - 1) mod 16 + wave / 2 of the chunk after
+    // the one that step kt - 1 is in; `row` from ts_row(ts_load(kt)).
+    auto ts_load = [&](int kt) { return ((kt - 1) & 7) * 2 + (wave >> 1); };
+    auto issue = [&](int S, int kt0, uint32_t row) {
+      const int kt = min(kt0, nk - 1);
+      const uint32_t st = g_lds_addr(sm[S]);
+      const bool sh = half && kt == nk - 1;
+      const uint32_t oc = (sh ? ln & 31 : ln) * 16, osc = ows - (sh ? (ln & 8) * 4 : 0);
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+        g_load16(acodes, min(oa[t] + (uint32_t)kt * 128, last_piece), st + kGTokAt + (4 * wave + t) * 1024);
+#pragma unroll
+      for (int s = 0; s < 4; ++s) g_load16(cp[s] + (size_t)kt * 1024, oc, st + kGCodeAt + (wave * 4 + s) * 1024);
+      g_load4(wsp + (size_t)kt * 64, osc, st + wave * 256);
+      issue_ts(((kt0 - 1) >> 3) + 1, ts_load(kt0), row);
+    };
+
+    f32x16 acc[2][4];
+#pragma unroll
+    for (int jn = 0; jn < 2; ++jn)
+#pragma unroll
+      for (int it = 0; it < 4; ++it)
+#pragma unroll
+        for (int v = 0; v < 16; ++v) acc[jn][it][v] = 0.f;
+
+    // Operands: 64 elements of two token tiles, and of the wave's two weight tiles.
+    struct Tokens {
+      u32x4 t[2][2];
+      uint32_t s[2];
+    };
+    struct Weights {
+      u32x4 w[2];
+      uint32_t s[2];
+    };
+    __syncthreads();  // the previous item's readers of the LDS are done
+    if (tid < kGM) s_row[tid] = row_at(min(tid, rows - 1)) * (uint32_t)ss;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) issue_ts(0, wave * 4 + i, ts_row(wave * 4 + i));
+    issue(0, 0, ts_row(ts_load(0)));
+    // AM token tiles in NP pairs; a step has NQ = 2 NP parts, part q = pair q % NP of half q / NP
+    auto run_k = [&](auto am_tag) {
+      constexpr int AM = decltype(am_tag)::value, NP = (AM + 1) / 2, NQ = 2 * NP;
+      Tokens tk[2];
+      Weights wt[2];
+      auto read = [&](int S, int kt, auto q_tag) {
+        constexpr int q = decltype(q_tag)::value, kh = q / NP, pr = q % NP;
+        const uint8_t* st = sm[S];
+        if (pr == 0) {
+#pragma unroll
+          for (int jn = 0; jn < 2; ++jn) {
+            const int s = wave * 4 + jn * 2 + (i32 >> 4);
+            wt[kh].w[jn] = *(const u32x4*)(st + kGCodeAt + s * 1024 + (2 * kh + g) * 256 + (i32 & 15) * 16);
+            wt[kh].s[jn] = st[s * 64 + (2 * kh + g) * 16 + (i32 & 15)];
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          if (2 * pr + u >= AM) continue;
+          const int r = (2 * pr + u) * 32 + i32, x = (r >> 1) & 7;
+          tk[q & 1].t[u][0] = *(const u32x4*)(st + kGTokAt + r * 128 + ((4 * kh + g) ^ x) * 16);
+          tk[q & 1].t[u][1] = *(const u32x4*)(st + kGTokAt + r * 128 + ((4 * kh + 2 + g) ^ x) * 16);
+          tk[q & 1].s[u] = s_ts[(kt >> 3) & 1][r * 8 + ((kt & 7) ^ ((r >> 3) & 7))];
+        }
+      };
+      auto multiply = [&](auto q_tag) {
+        constexpr int q = decltype(q_tag)::value, kh = q / NP, pr = q % NP;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          if (2 * pr + u >= AM) continue;
+          const int ts = (int)(tk[q & 1].s[u] >> (8 * g));
+#pragma unroll
+          for (int jn = 0; jn < 2; ++jn)
+            acc[jn][2 * pr + u] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                fp4_operand(wt[kh].w[jn]), fp8_operand(tk[q & 1].t[u][0], tk[q & 1].t[u][1]), acc[jn][2 * pr + u], 4, 0,
+                0, (int)wt[kh].s[jn], 2 * kh, ts);
+        }
+      };
+      using Q0 = std::integral_constant<int, 0>;
+      using Q1 = std::integral_constant<int, 1>;
+      // Part q's products over the reads of part q + 1.
+      auto part = [&](int S, int kt, auto q_tag) {
+        constexpr int q = decltype(q_tag)::value;
+        read(q + 1 < NQ ? S : S ^ 1, q + 1 < NQ ? kt : kt + 1, std::integral_constant<int, (q + 1) % NQ>{});
+        multiply(q_tag);
+        __builtin_amdgcn_sched_group_barrier(0x100, 12, 0);  // the LDS reads first,
+        __builtin_amdgcn_sched_group_barrier(0x008, 4, 0);   // then the matrix instructions
+        __builtin_amdgcn_sched_barrier(0);
+      };
+      auto upto_last = [&](int S, int kt) {
+        part(S, kt, Q0{});
+        if constexpr (NQ == 4) {
+          part(S, kt, Q1{});
+          part(S, kt, std::integral_constant<int, NQ - 2>{});
+        }
+      };
+      using QL = std::integral_constant<int, NQ - 1>;
+      g_wait_loads<0>();
+      lds_barrier();
+      issue(1, 1, ts_row(ts_load(1)));
+      read(0, 0, Q0{});
+      // A step: every part's operands are read under the products of the part before; ahead of
+      // the last part's products the next step's stage is complete and this one's read by every
+      // wave, so the loads of the step after the next go out (past the end: the last step's again,
+      // never read) and the next step's part 0 is read.
+      auto step = [&](int S, int kt) {
+        const uint32_t row = ts_row(ts_load(kt + 2));
+        upto_last(S, kt);
+        g_wait_loads<0>();
+        lds_barrier();
+        issue(S, kt + 2, row);
+        part(S, kt, QL{});
+      };
+      int kt = 0;
+      for (; kt + 2 < nk; kt += 2) {
+        step(0, kt);
+        step(1, kt + 1);
+      }
+      if (kt + 1 < nk) step(0, kt++);
+      const int S = kt & 1;  // the last step
+      if (half) {
+        if constexpr (NP == 2) read(S, kt, Q1{});
+        multiply(Q0{});
+        if constexpr (NP == 2) multiply(Q1{});
+      } else {
+        upto_last(S, kt);
+        multiply(QL{});
+      }
+      g_wait_loads<0>();  // those past the end too: the next item's may not be overtaken
+    };
+    switch (mtiles) {
+      case 1: run_k(std::integral_constant<int, 1>{}); break;
+      case 2: run_k(std::integral_constant<int, 2>{}); break;
+      case 3: run_k(std::integral_constant<int, 3>{}); break;
+      default: run_k(std::integral_constant<int, 4>{}); break;
+    }
+
+    // lane 32 g + i, value v: token row i, weight row 8 (v / 4) + 4 g + v % 4 of the tile's 32
+#pragma unroll
+    for (int it = 0; it < 4; ++it) {
+      if (it >= mtiles) continue;
+      const int r = it * 32 + i32;
+      if (MODE == 0) {
+        const int u0 = nt * 128 + wave * 32;
+        if (u0 >= p.f) continue;
+        float h[16];
+        uint32_t m = 0;
+#pragma unroll
+        for (int v = 0; v < 16; ++v) {
+          h[v] = g_swiglu(acc[0][it][v], acc[1][it][v]);
+          m = max(m, abs_bits(h[v]));
+        }
+        m = max(m, (uint32_t)__shfl_xor((int)m, 32));
+        const uint32_t s = mxfp8_scale_of(m);
+        const float sc = e8m0_value(s);
+        uint32_t w[4];
+#pragma unroll
+        for (int b = 0; b < 4; ++b) w[b] = mxfp8_pack4(h[4 * b], h[4 * b + 1], h[4 * b + 2], h[4 * b + 3], s, sc);
+        g_pair_rows(w);
+        if (r < rows) {
+          *(u32x4*)((uint8_t*)p.h + (size_t)(n0 + r) * p.f + u0 + 16 * g) = u32x4{w[0], w[1], w[2], w[3]};
+          if (g == 0) hscales[(size_t)(n0 + r) * mxfp8_scale_stride(p.f) + (u0 >> 5)] = (uint8_t)s;
+        }
+      } else {
+#pragma unroll
+        for (int jn = 0; jn < 2; ++jn) {
+          const int o0 = nt * 256 + wave * 64 + jn * 32;
+          if (o0 >= p.d) continue;
+          const size_t at = (size_t)(n0 + r) * p.d + o0;
+          if (YDT == MOE_F32) {
+            if (r < rows) {
+#pragma unroll
+              for (int b = 0; b < 4; ++b)
+                *(f32x4*)((float*)p.y + at + 8 * b + 4 * g) = f32x4{acc[jn][it][4 * b], acc[jn][it][4 * b + 1],
+                                                                    acc[jn][it][4 * b + 2], acc[jn][it][4 * b + 3]};
+            }
+          } else {
+            uint32_t a[4], c[4];  // elements 8 b + 4 g .. + 1 and + 2 .. + 3
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+              a[b] = (uint32_t)f32_to_bf16(acc[jn][it][4 * b]) | (uint32_t)f32_to_bf16(acc[jn][it][4 * b + 1]) << 16;
+              c[b] = (uint32_t)f32_to_bf16(acc[jn][it][4 * b + 2]) | (uint32_t)f32_to_bf16(acc[jn][it][4 * b + 3]) << 16;
+            }
+            g_pair_rows(a);
+            g_pair_rows(c);
+            if (r < rows) {
+              uint16_t* y = (uint16_t*)p.y + at + 16 * g;
+              *(u32x4*)y = u32x4{a[0], c[0], a[1], c[1]};
+              *(u32x4*)(y + 8) = u32x4{a[2], c[2], a[3], c[3]};
+            }
+          }
+        }
+      }
+    }
+  }
+}
+
+}  // namespace
+
+// Token rows and h rows are addressed with 32-bit byte offsets.
+bool ffn_mx8_gemm_supported(long long T, int k, int d, int f) {
+  return T * d <= (1ll << 32) && T * k * f <= (1ll << 32);
+}
+
+int launch_ffn_mx8_gemm(const FfnArgs& p, int T, int y_dtype, hipStream_t stream) {
+  const uint8_t* xs = (const uint8_t*)p.x + (size_t)T * p.d;
+  uint8_t* hs = (uint8_t*)p.h + (size_t)T * p.k * p.f;
+  // two workgroups a CU: the hand-off of a stage in one is covered by the other's products
+  const dim3 grid((num_cus() * 2 + 7) / 8 * 8), blk(256);
+  const int ntd = (p.d + 255) / 256;
+  const uint32_t last_h = (uint32_t)((size_t)T * p.k * p.f - 16);
+  hipLaunchKernelGGL((m8_tile<0, MOE_BF16>), grid, blk, 0, stream, p, xs, (uint32_t)((size_t)T * p.d - 16), hs, (p.f + 127) / 128);
+  MOE_LAUNCH_CHECK();
+  if (y_dtype == MOE_F32) hipLaunchKernelGGL((m8_tile<1, MOE_F32>), grid, blk, 0, stream, p, hs, last_h, nullptr, ntd);
+  else hipLaunchKernelGGL((m8_tile<1, MOE_BF16>), grid, blk, 0, stream, p, hs, last_h, nullptr, ntd);
+  MOE_LAUNCH_CHECK();
+  return MOE_OK;
+}
+
+}  // namespace moe
