@@ -43,6 +43,11 @@ constexpr int kGTsWords = kGM * 8;
 __device__ __forceinline__ uint32_t g_lds_addr(const void* p) {
   return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)p;
 }
+// LDS reads at a byte address + a constant.
+template <typename T>
+__device__ __forceinline__ T g_lds(uint32_t at, int off) {
+  return *(const __attribute__((address_space(3))) T*)(uintptr_t)(at + off);
+}
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"
 // 64 lanes x 16 (4) bytes from base + the lane's offset to consecutive LDS bytes from `lds` on.
@@ -121,6 +126,7 @@ void m8_tile(FfnArgs p, const uint8_t* ascales, uint32_t last_piece, uint8_t* hs
   const size_t fd = (size_t)p.f * p.d;
   const int ng = gridDim.x, per_xcd = ng >> 3;
   const int pos = (blockIdx.x & 7) * per_xcd + (blockIdx.x >> 3);
+  const uint32_t lds_sm = g_lds_addr(sm), lds_ts = g_lds_addr(s_ts);
   const uint8_t* acodes = (const uint8_t*)(MODE == 0 ? p.x : p.h);
 
   for (int j = pos; j < total_items; j += ng) {
@@ -140,72 +146,65 @@ void m8_tile(FfnArgs p, const uint8_t* ascales, uint32_t last_piece, uint8_t* hs
     if (!W) continue;
     const int n0 = p.offsets[e] + mt * kGM;
     const int rows = min(kGM, p.offsets[e + 1] - n0);
-    const int mtiles = (rows + 31) >> 5;
-
-    // this lane's sources: token rows (4 wave + t) * 8 + lane / 8, piece (lane & 7) unpermuted
-    uint32_t oa[4];
     int ln = lane;
-    asm volatile("" : "+v"(ln));  // keeps lane addresses out of the loop's live registers
-    const int g = ln >> 5, i32 = ln & 31;
+    asm volatile("" : "+v"(ln));  // keeps what follows from the lane out of the loops' live registers
+
+    // A wave loads 32 token rows (four loads of 8 rows, a lane's 16-byte piece permuted), the codes
+    // and the scales of its own four strips, and a load of the next token scale chunk: no branch,
+    // the same ten loads in each wave.  In a last step of 64 elements the second half of a code tile
+    // and of its scales does not exist (the first is read twice); the pieces of token rows past
+    // their end are other rows' or, at the buffer's last row, its last bytes.  None of that is used.
     auto row_at = [&](int r) { return (uint32_t)(MODE == 0 ? p.perm[n0 + r] / p.k : n0 + r); };
+    uint32_t oa[4];
 #pragma unroll
-    for (int t = 0; t < 4; ++t)
-      oa[t] = row_at(min((4 * wave + t) * 8 + (ln >> 3), rows - 1)) * (uint32_t)K +
-              ((ln & 7) ^ ((((4 * wave + t) * 8 + (ln >> 3)) >> 1) & 7)) * 16;
-    // strip s of the tile: 16 weight rows (past the matrix: row 0, its results dropped)
-    auto strip = [&](int s, size_t& co, size_t& so) {
-      int r0, m = 2;
-      if (MODE == 0) {
-        m = (s >> 1) & 1;
-        r0 = nt * 128 + (s >> 2) * 32 + (s & 1) * 16;
-      } else {
-        r0 = nt * 256 + s * 16;
-      }
-      if (r0 >= R) r0 = 0;
-      co = (size_t)m * (fd / 2) + (size_t)r0 * (K / 2);
-      so = 3 * (fd / 2) + (size_t)m * (fd / 32) + (size_t)r0 * (K / 32);
-    };
-    // A wave loads 32 token rows, the codes and the scales of its own four strips, and an eighth of
-    // a quarter of the next token scale chunk (a pair of waves the same): no branch, the same
-    // ten loads in each.  In a last step of 64 elements the second half of a code tile and of its scales does
-    // not exist (the first is read twice); the pieces of token rows past their end are other
-    // rows' or, at the buffer's last row, its last bytes.  None of that is used.
-    const uint8_t* cp[4];
-#pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      size_t co, so;
-      strip(wave * 4 + s, co, so);
-      cp[s] = W + co;
+    for (int t = 0; t < 4; ++t) {
+      const int r = (4 * wave + t) * 8 + (ln >> 3);
+      oa[t] = row_at(min(r, rows - 1)) * (uint32_t)K + ((ln & 7) ^ ((r >> 1) & 7)) * 16;
     }
-    const uint8_t* const wsp = W + 3 * (fd / 2);
-    uint32_t ows;
-    {
-      size_t co, so;
-      strip(wave * 4 + (ln >> 4), co, so);
-      ows = (uint32_t)(so - 3 * (fd / 2)) + (ln & 15) * 4;
-    }
+    // the wave's strips: 32 units of gate and of up, or 64 output channels (past the matrix:
+    // the first ones, their results dropped)
+    int r0 = MODE == 0 ? nt * 128 + wave * 32 : nt * 256 + wave * 64;
+    const bool out = r0 < R;
+    if (!out) r0 = 0;
+    const uint8_t* const wcodes = W + (MODE == 0 ? 0 : fd) + (size_t)r0 * (K / 2);
+    const uint8_t* const wscales = W + 3 * (fd / 2) + (MODE == 0 ? 0 : 2 * (fd / 32)) + (size_t)r0 * (K / 32);
+    const size_t strip = (size_t)K * 8, second = MODE == 0 ? fd / 2 : 2 * strip;
+    const uint32_t ows = ((ln >> 4) & 1) * (K / 2) + (ln >> 5) * (uint32_t)(MODE == 0 ? fd / 32 : K) + (ln & 15) * 4;
     // Load i of 16 of token scale chunk c: rows 8 i .. 8 i + 7 (words past a row's end: its last).
     auto ts_row = [&](int i) { return s_row[i * 8 + (ln >> 3)]; };
     auto issue_ts = [&](int c, int i, uint32_t row) {
       const int n = min(c * 8 + ((ln & 7) ^ (i & 7)), (ss >> 2) - 1);
-      g_load4(ascales, row + 4 * n, g_lds_addr(s_ts[c & 1]) + i * 256);
+      g_load4(ascales, row + 4 * n, lds_ts + (c & 1) * (kGTsWords * 4) + i * 256);
     };
-    // Stage S <- step kt (at most nk - 1), and load 2 (kt - 1) mod 16 + wave / 2 of the chunk after
+    // Stage kt0 mod 2 <- step kt0 (at most nk - 1), and load 2 (kt - 1) mod 16 + wave / 2 of the chunk after
     // the one that step kt - 1 is in; `row` from ts_row(ts_load(kt)).
     auto ts_load = [&](int kt) { return ((kt - 1) & 7) * 2 + (wave >> 1); };
-    auto issue = [&](int S, int kt0, uint32_t row) {
+    auto issue = [&](int kt0, uint32_t row) {
       const int kt = min(kt0, nk - 1);
-      const uint32_t st = g_lds_addr(sm[S]);
+      const uint32_t st = lds_sm + (kt0 & 1) * kGStage;
       const bool sh = half && kt == nk - 1;
       const uint32_t oc = (sh ? ln & 31 : ln) * 16, osc = ows - (sh ? (ln & 8) * 4 : 0);
+      const uint8_t* const c0 = wcodes + (size_t)kt * 1024;
 #pragma unroll
       for (int t = 0; t < 4; ++t)
         g_load16(acodes, min(oa[t] + (uint32_t)kt * 128, last_piece), st + kGTokAt + (4 * wave + t) * 1024);
 #pragma unroll
-      for (int s = 0; s < 4; ++s) g_load16(cp[s] + (size_t)kt * 1024, oc, st + kGCodeAt + (wave * 4 + s) * 1024);
-      g_load4(wsp + (size_t)kt * 64, osc, st + wave * 256);
+      for (int s = 0; s < 4; ++s)
+        g_load16(c0 + (s & 1) * strip + (s >> 1) * second, oc, st + kGCodeAt + (wave * 4 + s) * 1024);
+      g_load4(wscales + (size_t)kt * 64, osc, st + wave * 256);
       issue_ts(((kt0 - 1) >> 3) + 1, ts_load(kt0), row);
     };
+
+    // lane addresses of the operands: token pieces by half step and piece, codes, scales
+    const int g = ln >> 5, i32 = ln & 31;
+    uint32_t at_tok[2][2];
+#pragma unroll
+    for (int kh = 0; kh < 2; ++kh)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) at_tok[kh][c] = lds_sm + kGTokAt + i32 * 128 + ((4 * kh + 2 * c + g) ^ ((i32 >> 1) & 7)) * 16;
+    const uint32_t at_code = lds_sm + kGCodeAt + wave * 4096 + (i32 >> 4) * 1024 + g * 256 + (i32 & 15) * 16;
+    const uint32_t at_ws = lds_sm + wave * 256 + (i32 >> 4) * 64 + g * 16 + (i32 & 15);
+    const uint32_t at_ts = lds_ts + i32 * 32, x_ts = (i32 >> 3) * 4;
 
     f32x16 acc[2][4];
 #pragma unroll
@@ -229,37 +228,49 @@ void m8_tile(FfnArgs p, const uint8_t* ascales, uint32_t last_piece, uint8_t* hs
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < 4; ++i) issue_ts(0, wave * 4 + i, ts_row(wave * 4 + i));
-    issue(0, 0, ts_row(ts_load(0)));
-    // AM token tiles in NP pairs; a step has NQ = 2 NP parts, part q = pair q % NP of half q / NP
-    auto run_k = [&](auto am_tag) {
-      constexpr int AM = decltype(am_tag)::value, NP = (AM + 1) / 2, NQ = 2 * NP;
+    issue(0, ts_row(ts_load(0)));
+    // NP pairs of token tiles; a step has NQ = 2 NP parts, part q = pair q % NP of half q / NP
+    auto run_k = [&](auto np_tag) {
+      constexpr int NP = decltype(np_tag)::value, NQ = 2 * NP;
       Tokens tk[2];
       Weights wt[2];
-      auto read = [&](int S, int kt, auto q_tag) {
+      auto read = [&](int kt, auto q_tag) {
         constexpr int q = decltype(q_tag)::value, kh = q / NP, pr = q % NP;
-        const uint8_t* st = sm[S];
+        const uint32_t st = (kt & 1) * kGStage;
         if (pr == 0) {
 #pragma unroll
           for (int jn = 0; jn < 2; ++jn) {
-            const int s = wave * 4 + jn * 2 + (i32 >> 4);
-            wt[kh].w[jn] = *(const u32x4*)(st + kGCodeAt + s * 1024 + (2 * kh + g) * 256 + (i32 & 15) * 16);
-            wt[kh].s[jn] = st[s * 64 + (2 * kh + g) * 16 + (i32 & 15)];
+            wt[kh].w[jn] = g_lds<u32x4>(at_code + st, jn * 2048 + kh * 512);
+            wt[kh].s[jn] = g_lds<uint8_t>(at_ws + st, jn * 128 + kh * 32);
           }
         }
+        // word of row r, step n of the chunk: n ^ (r / 8) mod 8, r = 32 it + i32
+        const uint32_t ts = at_ts + ((kt >> 3) & 1) * (kGTsWords * 4) + (((kt & 7) * 4) ^ x_ts);
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          if (2 * pr + u >= AM) continue;
-          const int r = (2 * pr + u) * 32 + i32, x = (r >> 1) & 7;
-          tk[q & 1].t[u][0] = *(const u32x4*)(st + kGTokAt + r * 128 + ((4 * kh + g) ^ x) * 16);
-          tk[q & 1].t[u][1] = *(const u32x4*)(st + kGTokAt + r * 128 + ((4 * kh + 2 + g) ^ x) * 16);
-          tk[q & 1].s[u] = s_ts[(kt >> 3) & 1][r * 8 + ((kt & 7) ^ ((r >> 3) & 7))];
+          constexpr int it0 = 2 * pr;
+          tk[q & 1].t[u][0] = g_lds<u32x4>(at_tok[kh][0] + st, (it0 + u) * 4096);
+          tk[q & 1].t[u][1] = g_lds<u32x4>(at_tok[kh][1] + st, (it0 + u) * 4096);
+          tk[q & 1].s[u] = g_lds<uint32_t>(ts ^ (u * 16), (it0 + u) * 1024);
+        }
+      };
+      // The second half of a last step that has none: zeros (what was read may stand for NaN).
+      auto blank = [&](auto q_tag) {
+        constexpr int q = decltype(q_tag)::value, kh = q / NP, pr = q % NP;
+        if (kh == 0) return;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          if (pr == 0) wt[kh].w[u] = half ? u32x4{0u, 0u, 0u, 0u} : wt[kh].w[u];
+          if (pr == 0) wt[kh].s[u] = half ? 0u : wt[kh].s[u];
+          tk[q & 1].t[u][0] = half ? u32x4{0u, 0u, 0u, 0u} : tk[q & 1].t[u][0];
+          tk[q & 1].t[u][1] = half ? u32x4{0u, 0u, 0u, 0u} : tk[q & 1].t[u][1];
+          tk[q & 1].s[u] = half ? 0u : tk[q & 1].s[u];
         }
       };
       auto multiply = [&](auto q_tag) {
         constexpr int q = decltype(q_tag)::value, kh = q / NP, pr = q % NP;
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          if (2 * pr + u >= AM) continue;
           const int ts = (int)(tk[q & 1].s[u] >> (8 * g));
 #pragma unroll
           for (int jn = 0; jn < 2; ++jn)
@@ -269,72 +280,55 @@ void m8_tile(FfnArgs p, const uint8_t* ascales, uint32_t last_piece, uint8_t* hs
         }
       };
       using Q0 = std::integral_constant<int, 0>;
-      using Q1 = std::integral_constant<int, 1>;
+      using QL = std::integral_constant<int, NQ - 1>;
       // Part q's products over the reads of part q + 1.
-      auto part = [&](int S, int kt, auto q_tag) {
-        constexpr int q = decltype(q_tag)::value;
-        read(q + 1 < NQ ? S : S ^ 1, q + 1 < NQ ? kt : kt + 1, std::integral_constant<int, (q + 1) % NQ>{});
+      auto part = [&](int kt, auto q_tag, auto last_tag) {
+        constexpr int q = decltype(q_tag)::value, last = decltype(last_tag)::value;
+        using QN = std::integral_constant<int, (q + 1) % NQ>;
+        read(q + 1 < NQ ? kt : kt + 1, QN{});
         multiply(q_tag);
         __builtin_amdgcn_sched_group_barrier(0x100, 12, 0);  // the LDS reads first,
         __builtin_amdgcn_sched_group_barrier(0x008, 4, 0);   // then the matrix instructions
         __builtin_amdgcn_sched_barrier(0);
+        if constexpr (last) blank(QN{});
       };
-      auto upto_last = [&](int S, int kt) {
-        part(S, kt, Q0{});
+      auto upto_last = [&](int kt, auto last_tag) {
+        part(kt, Q0{}, last_tag);
         if constexpr (NQ == 4) {
-          part(S, kt, Q1{});
-          part(S, kt, std::integral_constant<int, NQ - 2>{});
+          part(kt, std::integral_constant<int, 1 % NQ>{}, last_tag);
+          part(kt, std::integral_constant<int, NQ - 2>{}, last_tag);
         }
       };
-      using QL = std::integral_constant<int, NQ - 1>;
       g_wait_loads<0>();
       lds_barrier();
-      issue(1, 1, ts_row(ts_load(1)));
-      read(0, 0, Q0{});
+      issue(1, ts_row(ts_load(1)));
+      read(0, Q0{});
       // A step: every part's operands are read under the products of the part before; ahead of
       // the last part's products the next step's stage is complete and this one's read by every
       // wave, so the loads of the step after the next go out (past the end: the last step's again,
       // never read) and the next step's part 0 is read.
-      auto step = [&](int S, int kt) {
+      for (int kt = 0; kt + 1 < nk; ++kt) {
         const uint32_t row = ts_row(ts_load(kt + 2));
-        upto_last(S, kt);
+        upto_last(kt, std::false_type{});
         g_wait_loads<0>();
         lds_barrier();
-        issue(S, kt + 2, row);
-        part(S, kt, QL{});
-      };
-      int kt = 0;
-      for (; kt + 2 < nk; kt += 2) {
-        step(0, kt);
-        step(1, kt + 1);
+        issue(kt + 2, row);
+        part(kt, QL{}, std::false_type{});
       }
-      if (kt + 1 < nk) step(0, kt++);
-      const int S = kt & 1;  // the last step
-      if (half) {
-        if constexpr (NP == 2) read(S, kt, Q1{});
-        multiply(Q0{});
-        if constexpr (NP == 2) multiply(Q1{});
-      } else {
-        upto_last(S, kt);
-        multiply(QL{});
-      }
+      upto_last(nk - 1, std::true_type{});
+      multiply(QL{});
       g_wait_loads<0>();  // those past the end too: the next item's may not be overtaken
     };
-    switch (mtiles) {
-      case 1: run_k(std::integral_constant<int, 1>{}); break;
-      case 2: run_k(std::integral_constant<int, 2>{}); break;
-      case 3: run_k(std::integral_constant<int, 3>{}); break;
-      default: run_k(std::integral_constant<int, 4>{}); break;
-    }
+    if (rows > 64) run_k(std::integral_constant<int, 2>{});
+    else run_k(std::integral_constant<int, 1>{});
 
     // lane 32 g + i, value v: token row i, weight row 8 (v / 4) + 4 g + v % 4 of the tile's 32
 #pragma unroll
     for (int it = 0; it < 4; ++it) {
-      if (it >= mtiles) continue;
+      if (it * 32 >= rows || !out) continue;
       const int r = it * 32 + i32;
       if (MODE == 0) {
-        const int u0 = nt * 128 + wave * 32;
-        if (u0 >= p.f) continue;
+        const int u0 = r0;
         float h[16];
         uint32_t m = 0;
 #pragma unroll
@@ -356,8 +350,7 @@ void m8_tile(FfnArgs p, const uint8_t* ascales, uint32_t last_piece, uint8_t* hs
       } else {
 #pragma unroll
         for (int jn = 0; jn < 2; ++jn) {
-          const int o0 = nt * 256 + wave * 64 + jn * 32;
-          if (o0 >= p.d) continue;
+          const int o0 = r0 + jn * 32;
           const size_t at = (size_t)(n0 + r) * p.d + o0;
           if (YDT == MOE_F32) {
             if (r < rows) {
