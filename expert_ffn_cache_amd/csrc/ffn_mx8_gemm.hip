@@ -30,15 +30,17 @@ namespace {
 constexpr int kGCodes = 16 * 1024;       // codes of a stage: strip s at s * 1024, slot 16 q + i
 constexpr int kGScales = 16 * 64;        // weight scales of a stage: strip s at s * 64
 
-constexpr int kGM = 128;                 // token rows of a tile
+constexpr int kGM = 256;                 // token rows of a tile
 // A stage: weight scales, token rows (row r at r * 128), codes.
 constexpr int kGTokAt = kGScales;
 constexpr int kGCodeAt = kGTokAt + kGM * 128;
 constexpr int kGStage = kGCodeAt + kGCodes;
-// Token scales come in chunks of 8 steps, two of them in LDS: row r's word of step n of a chunk at
-// word r * 8 + (n ^ (r / 8) mod 8).  One load brings 8 rows x 32 bytes; a word per row and step
+constexpr int kGStages = 3;
+constexpr int kGLoads = 8;  // loads of a wave per stage
+// Token scales come in chunks of 4 steps, two of them in LDS: row r's word of step n of a chunk at
+// word r * 4 + (n ^ (r / 16) mod 4).  One load brings 16 rows x 16 bytes; a word per row and step
 // instead would fetch a whole cache line for it (that alone cost half of the time).
-constexpr int kGTsWords = kGM * 8;
+constexpr int kGTsWords = kGM * 4;
 
 __device__ __forceinline__ uint32_t g_lds_addr(const void* p) {
   return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)p;
@@ -79,18 +81,17 @@ __device__ __forceinline__ void g_pair_rows(uint32_t (&w)[4]) {
 }
 
 template <int MODE, int YDT>  // MODE 0: gate/up (h out), 1: down (y out)
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2)))
+__global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2)))
 void m8_tile(FfnArgs p, const uint8_t* ascales, uint32_t last_piece, uint8_t* hscales, int n_ntiles) {
-  __shared__ __attribute__((aligned(1024))) uint8_t sm[2][kGStage];
+  __shared__ __attribute__((aligned(1024))) uint8_t sm[kGStages][kGStage];
   __shared__ int s_pref[kMaxE + 1];
-  __shared__ int s_part[4];
+  __shared__ int s_part[8];
   __shared__ __attribute__((aligned(256))) uint32_t s_ts[2][kGTsWords];
-  __shared__ uint32_t s_row[kGM];  // where the tile's token rows' scales start
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  {  // token tiles per expert and their prefix (E <= 1024: 4 experts per thread)
-    constexpr int PT = kMaxE / 256;
+  {  // token tiles per expert and their prefix (E <= 1024: 2 experts per thread)
+    constexpr int PT = kMaxE / 512;
     int c[PT], tot = 0;
 #pragma unroll
     for (int q = 0; q < PT; ++q) {
@@ -108,7 +109,7 @@ void m8_tile(FfnArgs p, const uint8_t* ascales, uint32_t last_piece, uint8_t* hs
     __syncthreads();
     int run = x - tot;
 #pragma unroll
-    for (int w = 0; w < 4; ++w)
+    for (int w = 0; w < 8; ++w)
       if (w < wave) run += s_part[w];
 #pragma unroll
     for (int q = 0; q < PT; ++q) {
@@ -126,6 +127,7 @@ void m8_tile(FfnArgs p, const uint8_t* ascales, uint32_t last_piece, uint8_t* hs
   const size_t fd = (size_t)p.f * p.d;
   const int ng = gridDim.x, per_xcd = ng >> 3;
   const int pos = (blockIdx.x & 7) * per_xcd + (blockIdx.x >> 3);
+  const int wn = wave & 3, wm = wave >> 2;
   const uint32_t lds_sm = g_lds_addr(sm), lds_ts = g_lds_addr(s_ts);
   const uint8_t* acodes = (const uint8_t*)(MODE == 0 ? p.x : p.h);
 
@@ -150,61 +152,74 @@ void m8_tile(FfnArgs p, const uint8_t* ascales, uint32_t last_piece, uint8_t* hs
     asm volatile("" : "+v"(ln));  // keeps what follows from the lane out of the loops' live registers
 
     // A wave loads 32 token rows (four loads of 8 rows, a lane's 16-byte piece permuted), the codes
-    // and the scales of its own four strips, and a load of the next token scale chunk: no branch,
-    // the same ten loads in each wave.  In a last step of 64 elements the second half of a code tile
-    // and of its scales does not exist (the first is read twice); the pieces of token rows past
-    // their end are other rows' or, at the buffer's last row, its last bytes.  None of that is used.
-    auto row_at = [&](int r) { return (uint32_t)(MODE == 0 ? p.perm[n0 + r] / p.k : n0 + r); };
+    // of two strips, the scales of four (waves w and w + 4 the same), and a load of a token scale
+    // chunk: no branch, the same eight loads in each wave.  In a last step of 64 elements the second
+    // half of a code tile and of its scales does not exist (the first is read twice); the pieces
+    // of token rows past their end are other rows' or, at the buffer's last row, its last bytes.
+    // None of that is used.
+    auto row_at = [&](int r) {
+      r = min(r, rows - 1);
+      return (uint32_t)(MODE == 0 ? p.perm[n0 + r] / p.k : n0 + r);
+    };
     uint32_t oa[4];
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
       const int r = (4 * wave + t) * 8 + (ln >> 3);
-      oa[t] = row_at(min(r, rows - 1)) * (uint32_t)K + ((ln & 7) ^ ((r >> 1) & 7)) * 16;
+      oa[t] = row_at(r) * (uint32_t)K + ((ln & 7) ^ ((r >> 1) & 7)) * 16;
     }
-    // the wave's strips: 32 units of gate and of up, or 64 output channels (past the matrix:
-    // the first ones, their results dropped)
-    int r0 = MODE == 0 ? nt * 128 + wave * 32 : nt * 256 + wave * 64;
-    const bool out = r0 < R;
-    if (!out) r0 = 0;
-    const uint8_t* const wcodes = W + (MODE == 0 ? 0 : fd) + (size_t)r0 * (K / 2);
-    const uint8_t* const wscales = W + 3 * (fd / 2) + (MODE == 0 ? 0 : 2 * (fd / 32)) + (size_t)r0 * (K / 32);
-    const size_t strip = (size_t)K * 8, second = MODE == 0 ? fd / 2 : 2 * strip;
+    const uint32_t ots = row_at(wave * 32 + (ln >> 2)) * (uint32_t)ss;
+    const uint32_t ots_step = row_at(wave * 32 + 16 + (ln >> 2)) * (uint32_t)ss - ots;
+    // first weight row of a group of four strips: 32 units of gate and of up, or 64 output channels
+    // (past the matrix: the first ones, their results dropped)
+    auto first_row = [&](int w) { return MODE == 0 ? nt * 128 + w * 32 : nt * 256 + w * 64; };
+    const bool out = first_row(wn) < R;
+    const int r0 = first_row(wn), rc = first_row(wave >> 1) < R ? first_row(wave >> 1) : 0, rs = out ? r0 : 0;
+    const size_t strip = (size_t)K * 8;
+    const uint8_t* const wcodes = W + (size_t)rc * (K / 2) + (MODE == 0 ? (wave & 1) * (fd / 2) : fd + (wave & 1) * 2 * strip);
+    const uint8_t* const wscales = W + 3 * (fd / 2) + (MODE == 0 ? 0 : 2 * (fd / 32)) + (size_t)rs * (K / 32);
     const uint32_t ows = ((ln >> 4) & 1) * (K / 2) + (ln >> 5) * (uint32_t)(MODE == 0 ? fd / 32 : K) + (ln & 15) * 4;
-    // Load i of 16 of token scale chunk c: rows 8 i .. 8 i + 7 (words past a row's end: its last).
-    auto ts_row = [&](int i) { return s_row[i * 8 + (ln >> 3)]; };
-    auto issue_ts = [&](int c, int i, uint32_t row) {
-      const int n = min(c * 8 + ((ln & 7) ^ (i & 7)), (ss >> 2) - 1);
-      g_load4(ascales, row + 4 * n, lds_ts + (c & 1) * (kGTsWords * 4) + i * 256);
+    // Load i of 2 of the wave's part of token scale chunk c: rows 32 wave + 16 i .. + 15 (words past
+    // a row's end: its last).
+    auto issue_ts = [&](int c, int i) {
+      const int n = min(c * 4 + ((ln & 3) ^ ((2 * wave + i) & 3)), (ss >> 2) - 1);
+      g_load4(ascales, ots + i * ots_step + 4 * n, lds_ts + (c & 1) * (kGTsWords * 4) + (wave * 2 + i) * 256);
     };
-    // Stage kt0 mod 2 <- step kt0 (at most nk - 1), and load 2 (kt - 1) mod 16 + wave / 2 of the chunk after
-    // the one that step kt - 1 is in; `row` from ts_row(ts_load(kt)).
-    auto ts_load = [&](int kt) { return ((kt - 1) & 7) * 2 + (wave >> 1); };
-    auto issue = [&](int kt0, uint32_t row) {
+    // The stage at LDS byte st <- step kt0 (at most nk - 1), and a load of the chunk that begins
+    // two to five steps later (each of its loads is issued twice): the eight loads, two a quarter.
+    auto issue = [&](uint32_t st, int kt0, auto quarter_tag) {
+      constexpr int qt = decltype(quarter_tag)::value;
       const int kt = min(kt0, nk - 1);
-      const uint32_t st = lds_sm + (kt0 & 1) * kGStage;
       const bool sh = half && kt == nk - 1;
-      const uint32_t oc = (sh ? ln & 31 : ln) * 16, osc = ows - (sh ? (ln & 8) * 4 : 0);
-      const uint8_t* const c0 = wcodes + (size_t)kt * 1024;
+      if constexpr (qt < 2) {
 #pragma unroll
-      for (int t = 0; t < 4; ++t)
-        g_load16(acodes, min(oa[t] + (uint32_t)kt * 128, last_piece), st + kGTokAt + (4 * wave + t) * 1024);
+        for (int t = 2 * qt; t < 2 * qt + 2; ++t)
+          g_load16(acodes, min(oa[t] + (uint32_t)kt * 128, last_piece), st + kGTokAt + (4 * wave + t) * 1024);
+      } else if constexpr (qt == 2) {
+        const uint32_t oc = (sh ? ln & 31 : ln) * 16;
 #pragma unroll
-      for (int s = 0; s < 4; ++s)
-        g_load16(c0 + (s & 1) * strip + (s >> 1) * second, oc, st + kGCodeAt + (wave * 4 + s) * 1024);
-      g_load4(wscales + (size_t)kt * 64, osc, st + wave * 256);
-      issue_ts(((kt0 - 1) >> 3) + 1, ts_load(kt0), row);
+        for (int s = 0; s < 2; ++s)
+          g_load16(wcodes + (size_t)kt * 1024 + s * strip, oc, st + kGCodeAt + (wave * 2 + s) * 1024);
+      } else {
+        g_load4(wscales + (size_t)kt * 64, ows - (sh ? (ln & 8) * 4 : 0), st + wn * 256);
+        issue_ts((kt0 + 2) >> 2, kt0 & 1);
+      }
     };
+    using I0 = std::integral_constant<int, 0>;
+    using I1 = std::integral_constant<int, 1>;
+    using I2 = std::integral_constant<int, 2>;
+    using I3 = std::integral_constant<int, 3>;
 
-    // lane addresses of the operands: token pieces by half step and piece, codes, scales
+    // lane addresses of the operands (within a stage): token pieces by half step and piece, codes,
+    // scales; token tile it of the wave is rows 64 it + 32 wm .. + 31
     const int g = ln >> 5, i32 = ln & 31;
     uint32_t at_tok[2][2];
 #pragma unroll
     for (int kh = 0; kh < 2; ++kh)
 #pragma unroll
-      for (int c = 0; c < 2; ++c) at_tok[kh][c] = lds_sm + kGTokAt + i32 * 128 + ((4 * kh + 2 * c + g) ^ ((i32 >> 1) & 7)) * 16;
-    const uint32_t at_code = lds_sm + kGCodeAt + wave * 4096 + (i32 >> 4) * 1024 + g * 256 + (i32 & 15) * 16;
-    const uint32_t at_ws = lds_sm + wave * 256 + (i32 >> 4) * 64 + g * 16 + (i32 & 15);
-    const uint32_t at_ts = lds_ts + i32 * 32, x_ts = (i32 >> 3) * 4;
+      for (int c = 0; c < 2; ++c) at_tok[kh][c] = kGTokAt + (wm * 32 + i32) * 128 + ((4 * kh + 2 * c + g) ^ ((i32 >> 1) & 7)) * 16;
+    const uint32_t at_code = kGCodeAt + wn * 4096 + (i32 >> 4) * 1024 + g * 256 + (i32 & 15) * 16;
+    const uint32_t at_ws = wn * 256 + (i32 >> 4) * 64 + g * 16 + (i32 & 15);
+    const uint32_t at_ts = lds_ts + (wm * 32 + i32) * 16, x_ts = ((2 * wm + (i32 >> 4)) & 3) * 4;
 
     f32x16 acc[2][4];
 #pragma unroll
@@ -224,19 +239,22 @@ void m8_tile(FfnArgs p, const uint8_t* ascales, uint32_t last_piece, uint8_t* hs
       uint32_t s[2];
     };
     __syncthreads();  // the previous item's readers of the LDS are done
-    if (tid < kGM) s_row[tid] = row_at(min(tid, rows - 1)) * (uint32_t)ss;
-    __syncthreads();
+    issue_ts(0, 0);
+    issue_ts(0, 1);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) issue_ts(0, wave * 4 + i, ts_row(wave * 4 + i));
-    issue(0, ts_row(ts_load(0)));
-    // NP pairs of token tiles; a step has NQ = 2 NP parts, part q = pair q % NP of half q / NP
-    auto run_k = [&](auto np_tag) {
-      constexpr int NP = decltype(np_tag)::value, NQ = 2 * NP;
+    for (int i = 0; i < 2; ++i) {
+      issue(lds_sm + i * kGStage, i, I0{});
+      issue(lds_sm + i * kGStage, i, I1{});
+      issue(lds_sm + i * kGStage, i, I2{});
+      issue(lds_sm + i * kGStage, i, I3{});
+    }
+    // AM token tiles in NP pairs; a step has NQ = 2 NP parts, part q = pair q % NP of half q / NP
+    auto run_k = [&](auto am_tag) {
+      constexpr int AM = decltype(am_tag)::value, NP = (AM + 1) / 2, NQ = 2 * NP;
       Tokens tk[2];
       Weights wt[2];
-      auto read = [&](int kt, auto q_tag) {
+      auto read = [&](uint32_t st, int kt, auto q_tag) {
         constexpr int q = decltype(q_tag)::value, kh = q / NP, pr = q % NP;
-        const uint32_t st = (kt & 1) * kGStage;
         if (pr == 0) {
 #pragma unroll
           for (int jn = 0; jn < 2; ++jn) {
@@ -244,14 +262,14 @@ void m8_tile(FfnArgs p, const uint8_t* ascales, uint32_t last_piece, uint8_t* hs
             wt[kh].s[jn] = g_lds<uint8_t>(at_ws + st, jn * 128 + kh * 32);
           }
         }
-        // word of row r, step n of the chunk: n ^ (r / 8) mod 8, r = 32 it + i32
-        const uint32_t ts = at_ts + ((kt >> 3) & 1) * (kGTsWords * 4) + (((kt & 7) * 4) ^ x_ts);
+        // word of row r, step n of the chunk: n ^ (r / 16) mod 4, r = 64 it + 32 wm + i32
+        const uint32_t ts = at_ts + ((kt >> 2) & 1) * (kGTsWords * 4) + (((kt & 3) * 4) ^ x_ts);
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          constexpr int it0 = 2 * pr;
-          tk[q & 1].t[u][0] = g_lds<u32x4>(at_tok[kh][0] + st, (it0 + u) * 4096);
-          tk[q & 1].t[u][1] = g_lds<u32x4>(at_tok[kh][1] + st, (it0 + u) * 4096);
-          tk[q & 1].s[u] = g_lds<uint32_t>(ts ^ (u * 16), (it0 + u) * 1024);
+          if (2 * pr + u >= AM) continue;
+          tk[q & 1].t[u][0] = g_lds<u32x4>(at_tok[kh][0] + st, (2 * pr + u) * 8192);
+          tk[q & 1].t[u][1] = g_lds<u32x4>(at_tok[kh][1] + st, (2 * pr + u) * 8192);
+          tk[q & 1].s[u] = g_lds<uint32_t>(ts, (2 * pr + u) * 1024);
         }
       };
       // The second half of a last step that has none: zeros (what was read may stand for NaN).
@@ -262,6 +280,7 @@ void m8_tile(FfnArgs p, const uint8_t* ascales, uint32_t last_piece, uint8_t* hs
         for (int u = 0; u < 2; ++u) {
           if (pr == 0) wt[kh].w[u] = half ? u32x4{0u, 0u, 0u, 0u} : wt[kh].w[u];
           if (pr == 0) wt[kh].s[u] = half ? 0u : wt[kh].s[u];
+          if (2 * pr + u >= AM) continue;
           tk[q & 1].t[u][0] = half ? u32x4{0u, 0u, 0u, 0u} : tk[q & 1].t[u][0];
           tk[q & 1].t[u][1] = half ? u32x4{0u, 0u, 0u, 0u} : tk[q & 1].t[u][1];
           tk[q & 1].s[u] = half ? 0u : tk[q & 1].s[u];
@@ -271,6 +290,7 @@ void m8_tile(FfnArgs p, const uint8_t* ascales, uint32_t last_piece, uint8_t* hs
         constexpr int q = decltype(q_tag)::value, kh = q / NP, pr = q % NP;
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
+          if (2 * pr + u >= AM) continue;
           const int ts = (int)(tk[q & 1].s[u] >> (8 * g));
 #pragma unroll
           for (int jn = 0; jn < 2; ++jn)
@@ -281,52 +301,75 @@ void m8_tile(FfnArgs p, const uint8_t* ascales, uint32_t last_piece, uint8_t* hs
       };
       using Q0 = std::integral_constant<int, 0>;
       using QL = std::integral_constant<int, NQ - 1>;
-      // Part q's products over the reads of part q + 1.
-      auto part = [&](int kt, auto q_tag, auto last_tag) {
-        constexpr int q = decltype(q_tag)::value, last = decltype(last_tag)::value;
-        using QN = std::integral_constant<int, (q + 1) % NQ>;
-        read(q + 1 < NQ ? kt : kt + 1, QN{});
-        multiply(q_tag);
-        __builtin_amdgcn_sched_group_barrier(0x100, 12, 0);  // the LDS reads first,
-        __builtin_amdgcn_sched_group_barrier(0x008, 4, 0);   // then the matrix instructions
+      // Part q's products over the reads of part q + 1, `loads` issued between.
+      auto part = [&](uint32_t st, int kt, auto q_tag, auto loads) {
+        constexpr int q = decltype(q_tag)::value;
+        read(st, kt, std::integral_constant<int, (q + 1) % NQ>{});
         __builtin_amdgcn_sched_barrier(0);
-        if constexpr (last) blank(QN{});
+        loads();
+        multiply(q_tag);
+        __builtin_amdgcn_sched_barrier(0);
       };
-      auto upto_last = [&](int kt, auto last_tag) {
-        part(kt, Q0{}, last_tag);
-        if constexpr (NQ == 4) {
-          part(kt, std::integral_constant<int, 1 % NQ>{}, last_tag);
-          part(kt, std::integral_constant<int, NQ - 2>{}, last_tag);
-        }
-      };
-      g_wait_loads<0>();
+      using QL = std::integral_constant<int, NQ - 1>;
+      using Q1 = std::integral_constant<int, 1 % NQ>;
+      using Q2 = std::integral_constant<int, (NQ + 2) % NQ>;
+      uint32_t st = lds_sm, st1 = lds_sm + kGStage, st2 = lds_sm + 2 * kGStage;
+      issue(st2, 2, I0{});
+      if constexpr (NQ == 2) issue(st2, 2, I1{});
+      g_wait_loads<kGLoads + 8 / NQ>();
       lds_barrier();
-      issue(1, ts_row(ts_load(1)));
-      read(0, Q0{});
+      read(st, 0, Q0{});
       // A step: every part's operands are read under the products of the part before; ahead of
       // the last part's products the next step's stage is complete and this one's read by every
-      // wave, so the loads of the step after the next go out (past the end: the last step's again,
-      // never read) and the next step's part 0 is read.
+      // wave, and from there on to the same place of the next step the loads of the third step from
+      // here go out (past the end: the last step's again, never read), some in each part: all at
+      // once they hold a wave up until the address unit has taken them.
       for (int kt = 0; kt + 1 < nk; ++kt) {
-        const uint32_t row = ts_row(ts_load(kt + 2));
-        upto_last(kt, std::false_type{});
-        g_wait_loads<0>();
+        if constexpr (NQ == 4) {
+          part(st, kt, Q0{}, [&] { issue(st2, kt + 2, I1{}); });
+          part(st, kt, Q1{}, [&] { issue(st2, kt + 2, I2{}); });
+          part(st, kt, Q2{}, [&] { issue(st2, kt + 2, I3{}); });
+        } else {
+          part(st, kt, Q0{}, [&] {
+            issue(st2, kt + 2, I2{});
+            issue(st2, kt + 2, I3{});
+          });
+        }
+        g_wait_loads<kGLoads>();
         lds_barrier();
-        issue(kt + 2, row);
-        part(kt, QL{}, std::false_type{});
+        part(st1, kt + 1, QL{}, [&] {
+          issue(st, kt + 3, I0{});
+          if constexpr (NQ == 2) issue(st, kt + 3, I1{});
+        });
+        const uint32_t t = st;
+        st = st1;
+        st1 = st2;
+        st2 = t;
       }
-      upto_last(nk - 1, std::true_type{});
+      auto none = [] {};
+      part(st, nk - 1, Q0{}, none);
+      blank(Q1{});
+      if constexpr (NQ == 4) {
+        part(st, nk - 1, Q1{}, none);
+        blank(Q2{});
+        part(st, nk - 1, Q2{}, none);
+        blank(QL{});
+      }
       multiply(QL{});
       g_wait_loads<0>();  // those past the end too: the next item's may not be overtaken
     };
-    if (rows > 64) run_k(std::integral_constant<int, 2>{});
-    else run_k(std::integral_constant<int, 1>{});
+    switch ((rows + 63) >> 6) {
+      case 1: run_k(std::integral_constant<int, 1>{}); break;
+      case 2: run_k(std::integral_constant<int, 2>{}); break;
+      case 3: run_k(std::integral_constant<int, 3>{}); break;
+      default: run_k(std::integral_constant<int, 4>{}); break;
+    }
 
     // lane 32 g + i, value v: token row i, weight row 8 (v / 4) + 4 g + v % 4 of the tile's 32
 #pragma unroll
     for (int it = 0; it < 4; ++it) {
-      if (it * 32 >= rows || !out) continue;
-      const int r = it * 32 + i32;
+      if (it * 64 + wm * 32 >= rows || !out) continue;
+      const int r = it * 64 + wm * 32 + i32;
       if (MODE == 0) {
         const int u0 = r0;
         float h[16];
@@ -390,8 +433,7 @@ bool ffn_mx8_gemm_supported(long long T, int k, int d, int f) {
 int launch_ffn_mx8_gemm(const FfnArgs& p, int T, int y_dtype, hipStream_t stream) {
   const uint8_t* xs = (const uint8_t*)p.x + (size_t)T * p.d;
   uint8_t* hs = (uint8_t*)p.h + (size_t)T * p.k * p.f;
-  // two workgroups a CU: the hand-off of a stage in one is covered by the other's products
-  const dim3 grid((num_cus() * 2 + 7) / 8 * 8), blk(256);
+  const dim3 grid((num_cus() + 7) / 8 * 8), blk(512);
   const int ntd = (p.d + 255) / 256;
   const uint32_t last_h = (uint32_t)((size_t)T * p.k * p.f - 16);
   hipLaunchKernelGGL((m8_tile<0, MOE_BF16>), grid, blk, 0, stream, p, xs, (uint32_t)((size_t)T * p.d - 16), hs, (p.f + 127) / 128);
