@@ -104,11 +104,17 @@ static size_t ffn_h_bytes(int T, int k, int f, int act_dtype) {
   return (size_t)T * k * f * (act_dtype == MOE_F32 ? 4 : 2);
 }
 
+// The least workspace of a call: h, and with MXFP8 activations the grouped GEMM's plan behind it.
+static size_t ffn_need_bytes(int T, int k, int f, int act_dtype) {
+  const size_t h = ffn_h_bytes(T, k, f, act_dtype);
+  return act_dtype == MOE_MXFP8 ? (h + 255) / 256 * 256 + ffn_mx8_plan_bytes((long long)T * k, kMaxE) : h;
+}
+
 // Up to kMxMaxRows tokens with bf16 activations, room for h as tagged 8-byte entries (4 bytes
 // per unit), which lets MXFP4 calls run both projections in one launch.
 extern "C" size_t moe_expert_ffn_workspace_bytes(int T, int k, int f, int act_dtype) {
   if (T <= 0 || k <= 0 || f <= 0) return 256;
-  if (act_dtype == MOE_MXFP8) return (ffn_h_bytes(T, k, f, act_dtype) + 255) / 256 * 256;
+  if (act_dtype == MOE_MXFP8) return (ffn_need_bytes(T, k, f, act_dtype) + 255) / 256 * 256;
   const size_t el = act_dtype == MOE_F32 ? 4 : T <= kMxMaxRows ? 4 : 2;
   return ((size_t)T * k * f * el + 255) / 256 * 256;
 }
@@ -142,7 +148,7 @@ extern "C" int moe_expert_ffn(const void* x, int act_dtype, const int32_t* perm,
   if (!x || !perm || !offsets || !arena || !ws || !y_perm) return MOE_EINVAL;
   if (!moe_aligned16(x) || !moe_aligned16(arena) || !moe_aligned16(ws) || !moe_aligned16(y_perm))
     return MOE_EINVAL;
-  if (ws_bytes < ffn_h_bytes(T, k, f, act_dtype)) return MOE_EINVAL;
+  if (ws_bytes < ffn_need_bytes(T, k, f, act_dtype)) return MOE_EINVAL;
 
   FfnArgs p{x, perm, offsets, k, E, d, f, expert_slot, (const char*)arena, entry_stride,
             expert_mask, slot_key, key_base, ws, y_perm, status};
@@ -256,7 +262,7 @@ extern "C" int moe_expert_ffn_noalloc(const void* x, int act_dtype, const int32_
                                       const int32_t* slot_key, int key_base, void* y_perm,
                                       int y_dtype, int path, int32_t* status, hipStream_t stream) {
   if (T < 0 || k <= 0 || f <= 0) return MOE_EINVAL;
-  if (ffn_h_bytes(T, k, f, act_dtype) > kScratchBytes) return MOE_ETOOBIG;
+  if (ffn_need_bytes(T, k, f, act_dtype) > kScratchBytes) return MOE_ETOOBIG;
   void* ws = scratch_ptr();
   if (!ws) return MOE_EHIP;
   return moe_expert_ffn(x, act_dtype, perm, offsets, T, k, E, d, f, expert_slot, arena,

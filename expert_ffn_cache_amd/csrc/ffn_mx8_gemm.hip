@@ -30,17 +30,15 @@ namespace {
 constexpr int kGCodes = 16 * 1024;       // codes of a stage: strip s at s * 1024, slot 16 q + i
 constexpr int kGScales = 16 * 64;        // weight scales of a stage: strip s at s * 64
 
-constexpr int kGM = 256;                 // token rows of a tile
+constexpr int kGM = 128;                 // token rows of a tile
 // A stage: weight scales, token rows (row r at r * 128), codes.
 constexpr int kGTokAt = kGScales;
 constexpr int kGCodeAt = kGTokAt + kGM * 128;
 constexpr int kGStage = kGCodeAt + kGCodes;
-constexpr int kGStages = 3;
-constexpr int kGLoads = 8;  // loads of a wave per stage
-// Token scales come in chunks of 4 steps, two of them in LDS: row r's word of step n of a chunk at
-// word r * 4 + (n ^ (r / 16) mod 4).  One load brings 16 rows x 16 bytes; a word per row and step
+// Token scales come in chunks of 8 steps, two of them in LDS: row r's word of step n of a chunk at
+// word r * 8 + (n ^ (r / 8) mod 8).  One load brings 8 rows x 32 bytes; a word per row and step
 // instead would fetch a whole cache line for it (that alone cost half of the time).
-constexpr int kGTsWords = kGM * 4;
+constexpr int kGTsWords = kGM * 8;
 
 __device__ __forceinline__ uint32_t g_lds_addr(const void* p) {
   return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)p;
@@ -80,146 +78,190 @@ __device__ __forceinline__ void g_pair_rows(uint32_t (&w)[4]) {
   w[0] = a[0]; w[1] = a[1]; w[2] = b[0]; w[3] = b[1];
 }
 
+// The plan of a call, in its workspace: a queue counter per mode and XCD (64 bytes apart), the
+// first token tile of each XCD's share, and the token tiles in expert order.
+constexpr int kPlanShares = 256, kPlanTiles = 512;  // in words
+struct PlanTile {
+  int e, n0, rows, pad;  // expert, first grouped row, rows (at most kGM)
+};
+__host__ __device__ constexpr int plan_counter(int mode, int xcd) { return 16 * (8 * mode + xcd); }
+
+// One workgroup.  Shares are cut by cost, a tile's being its 32-row products and two for what an
+// item costs beside them.
+__global__ __launch_bounds__(kMaxE) void m8_plan(FfnArgs p, int* plan) {
+  __shared__ int s_cnt[kMaxE / 64];
+  __shared__ long long s_cost[kMaxE / 64];
+  const int e = threadIdx.x, lane = e & 63, wave = e >> 6;
+  const int n0 = e < p.E && active(p, e) ? p.offsets[e] : 0;
+  const int n = e < p.E && active(p, e) ? p.offsets[e + 1] - n0 : 0;
+  const int tiles = (n + kGM - 1) / kGM;
+  auto cost_of = [](int rows) { return (rows + 31) / 32 + 2; };
+  const long long cost = tiles ? (long long)(tiles - 1) * cost_of(kGM) + cost_of(n - (tiles - 1) * kGM) : 0;
+  int x = tiles;
+  long long y = cost;
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) {
+    const int u = __shfl_up(x, off);
+    const long long v = __shfl_up(y, off);
+    if (lane >= off) {
+      x += u;
+      y += v;
+    }
+  }
+  if (lane == 63) {
+    s_cnt[wave] = x;
+    s_cost[wave] = y;
+  }
+  if (e < 16) plan[16 * e] = 0;
+  __syncthreads();
+  int first = x - tiles, all = 0;
+  long long before = y - cost, total = 0;
+  for (int w = 0; w < kMaxE / 64; ++w) {
+    if (w < wave) {
+      first += s_cnt[w];
+      before += s_cost[w];
+    }
+    all += s_cnt[w];
+    total += s_cost[w];
+  }
+  if (e <= 8) plan[kPlanShares + e] = e == 0 ? 0 : all;
+  __syncthreads();
+  PlanTile* t = (PlanTile*)(plan + kPlanTiles);
+  for (int m = 0; m < tiles; ++m) {
+    const int rows = min(kGM, n - m * kGM);
+    t[first + m] = PlanTile{e, n0 + m * kGM, rows, 0};
+    for (int c = 1; c < 8; ++c) {  // the share that begins in this tile's cost begins with it
+      const long long cut = total * c / 8;
+      if (cut >= before && cut < before + cost_of(rows)) plan[kPlanShares + c] = first + m;
+    }
+    before += cost_of(rows);
+  }
+}
+
 template <int MODE, int YDT>  // MODE 0: gate/up (h out), 1: down (y out)
-__global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2)))
-void m8_tile(FfnArgs p, const uint8_t* ascales, uint32_t last_piece, uint8_t* hscales, int n_ntiles) {
-  __shared__ __attribute__((aligned(1024))) uint8_t sm[kGStages][kGStage];
-  __shared__ int s_pref[kMaxE + 1];
-  __shared__ int s_part[8];
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2)))
+void m8_tile(FfnArgs p, const uint8_t* ascales, uint32_t last_piece, uint8_t* hscales, int n_ntiles, int* plan) {
+  __shared__ __attribute__((aligned(1024))) uint8_t sm[2][kGStage];
+  __shared__ int s_item[2];  // an XCD's share and the item in its queue, -1: none left
   __shared__ __attribute__((aligned(256))) uint32_t s_ts[2][kGTsWords];
+  __shared__ uint32_t s_row[kGM];  // where the tile's token rows' scales start
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  {  // token tiles per expert and their prefix (E <= 1024: 2 experts per thread)
-    constexpr int PT = kMaxE / 512;
-    int c[PT], tot = 0;
-#pragma unroll
-    for (int q = 0; q < PT; ++q) {
-      const int e = tid * PT + q;
-      c[q] = e < p.E && active(p, e) ? (p.offsets[e + 1] - p.offsets[e] + kGM - 1) / kGM : 0;
-      tot += c[q];
-    }
-    int x = tot;
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
-      const int y = __shfl_up(x, off);
-      if (lane >= off) x += y;
-    }
-    if (lane == 63) s_part[wave] = x;
-    __syncthreads();
-    int run = x - tot;
-#pragma unroll
-    for (int w = 0; w < 8; ++w)
-      if (w < wave) run += s_part[w];
-#pragma unroll
-    for (int q = 0; q < PT; ++q) {
-      const int e = tid * PT + q;
-      if (e < p.E) s_pref[e] = run;
-      run += c[q];
-      if (e == p.E - 1) s_pref[p.E] = run;
-    }
-    __syncthreads();
-  }
-  const int total_items = s_pref[p.E] * n_ntiles;
   const int K = MODE == 0 ? p.d : p.f, R = MODE == 0 ? p.f : p.d;
   const int nk = (K + 127) >> 7, ss = mxfp8_scale_stride(K);
   const bool half = (K & 127) != 0;  // the last step holds 64 elements
   const size_t fd = (size_t)p.f * p.d;
-  const int ng = gridDim.x, per_xcd = ng >> 3;
-  const int pos = (blockIdx.x & 7) * per_xcd + (blockIdx.x >> 3);
-  const int wn = wave & 3, wm = wave >> 2;
   const uint32_t lds_sm = g_lds_addr(sm), lds_ts = g_lds_addr(s_ts);
   const uint8_t* acodes = (const uint8_t*)(MODE == 0 ? p.x : p.h);
 
-  for (int j = pos; j < total_items; j += ng) {
-    const int q = j / n_ntiles;
-    int lo = 0, hi = p.E;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (s_pref[mid] <= q) lo = mid; else hi = mid - 1;
+  // Items of this XCD's share first, then of the others', so no workgroup stops early; a share's
+  // queue runs over its token tiles, four of them to a weight tile.  Thread 0 draws the next item
+  // while the current one is computed.
+  const int* const share = plan + kPlanShares;
+  const PlanTile* const tiles = (const PlanTile*)(plan + kPlanTiles);
+  auto draw = [&](int q) { return atomicAdd(plan + plan_counter(MODE, q & 7), 1); };
+  auto settle = [&](int q, int j) {  // item j of share q if there is one, else of the next share that has
+    const int q0 = blockIdx.x & 7;
+    while (j >= (share[(q & 7) + 1] - share[q & 7]) * n_ntiles) {
+      if (++q >= q0 + 8) {
+        q = -1;
+        break;
+      }
+      j = draw(q);
     }
-    const int e = lo;
-    const int m_e = s_pref[e + 1] - s_pref[e];
-    const int local = j - s_pref[e] * n_ntiles;
-    const int grp = local / (4 * n_ntiles), first_m = grp * 4;
-    const int gsz = min(4, m_e - first_m), in = local - grp * 4 * n_ntiles;
-    const int nt = in / gsz, mt = first_m + (in - nt * gsz);
-    const uint8_t* W = (const uint8_t*)entry_of(p, e);
-    if (!W) continue;
-    const int n0 = p.offsets[e] + mt * kGM;
-    const int rows = min(kGM, p.offsets[e + 1] - n0);
+    s_item[0] = q;
+    s_item[1] = j;
+  };
+  int next_q = blockIdx.x & 7, next_j = 0;
+  if (tid == 0) settle(next_q, draw(next_q));
+  __syncthreads();
+
+  for (;;) {
+    const int q = s_item[0], j = s_item[1];
+    if (q < 0) return;
+    const int m_0 = share[q & 7], m_n = share[(q & 7) + 1] - m_0;
+    const int grp = j / (4 * n_ntiles), gsz = min(4, m_n - grp * 4), in = j - grp * 4 * n_ntiles;
+    const int nt = in / gsz;
+    const PlanTile tile = tiles[m_0 + grp * 4 + (in - nt * gsz)];
+    const int n0 = tile.n0, rows = tile.rows;
+    const uint8_t* W = (const uint8_t*)entry_of(p, tile.e);
+    __syncthreads();  // the item is read, and the previous one's readers of the LDS are done
+    if (tid == 0) {
+      next_q = q;
+      next_j = draw(q);
+    }
+    if (!W) {
+      if (tid == 0) settle(next_q, next_j);
+      __syncthreads();
+      continue;
+    }
     int ln = lane;
     asm volatile("" : "+v"(ln));  // keeps what follows from the lane out of the loops' live registers
 
     // A wave loads 32 token rows (four loads of 8 rows, a lane's 16-byte piece permuted), the codes
-    // of two strips, the scales of four (waves w and w + 4 the same), and a load of a token scale
-    // chunk: no branch, the same eight loads in each wave.  In a last step of 64 elements the second
-    // half of a code tile and of its scales does not exist (the first is read twice); the pieces
-    // of token rows past their end are other rows' or, at the buffer's last row, its last bytes.
-    // None of that is used.
-    auto row_at = [&](int r) {
-      r = min(r, rows - 1);
-      return (uint32_t)(MODE == 0 ? p.perm[n0 + r] / p.k : n0 + r);
-    };
+    // and the scales of its own four strips, and a load of the next token scale chunk: no branch,
+    // the same ten loads in each wave.  In a last step of 64 elements the second half of a code tile
+    // and of its scales does not exist (the first is read twice); the pieces of token rows past
+    // their end are other rows' or, at the buffer's last row, its last bytes.  None of that is used.
+    auto row_at = [&](int r) { return (uint32_t)(MODE == 0 ? p.perm[n0 + r] / p.k : n0 + r); };
     uint32_t oa[4];
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
       const int r = (4 * wave + t) * 8 + (ln >> 3);
-      oa[t] = row_at(r) * (uint32_t)K + ((ln & 7) ^ ((r >> 1) & 7)) * 16;
+      oa[t] = row_at(min(r, rows - 1)) * (uint32_t)K + ((ln & 7) ^ ((r >> 1) & 7)) * 16;
     }
-    const uint32_t ots = row_at(wave * 32 + (ln >> 2)) * (uint32_t)ss;
-    const uint32_t ots_step = row_at(wave * 32 + 16 + (ln >> 2)) * (uint32_t)ss - ots;
-    // first weight row of a group of four strips: 32 units of gate and of up, or 64 output channels
-    // (past the matrix: the first ones, their results dropped)
-    auto first_row = [&](int w) { return MODE == 0 ? nt * 128 + w * 32 : nt * 256 + w * 64; };
-    const bool out = first_row(wn) < R;
-    const int r0 = first_row(wn), rc = first_row(wave >> 1) < R ? first_row(wave >> 1) : 0, rs = out ? r0 : 0;
-    const size_t strip = (size_t)K * 8;
-    const uint8_t* const wcodes = W + (size_t)rc * (K / 2) + (MODE == 0 ? (wave & 1) * (fd / 2) : fd + (wave & 1) * 2 * strip);
-    const uint8_t* const wscales = W + 3 * (fd / 2) + (MODE == 0 ? 0 : 2 * (fd / 32)) + (size_t)rs * (K / 32);
+    // the wave's strips: 32 units of gate and of up, or 64 output channels (past the matrix:
+    // the first ones, their results dropped)
+    int r0 = MODE == 0 ? nt * 128 + wave * 32 : nt * 256 + wave * 64;
+    const bool out = r0 < R;
+    if (!out) r0 = 0;
+    const uint8_t* const wcodes = W + (MODE == 0 ? 0 : fd) + (size_t)r0 * (K / 2);
+    const uint8_t* const wscales = W + 3 * (fd / 2) + (MODE == 0 ? 0 : 2 * (fd / 32)) + (size_t)r0 * (K / 32);
+    const size_t strip = (size_t)K * 8, second = MODE == 0 ? fd / 2 : 2 * strip;
     const uint32_t ows = ((ln >> 4) & 1) * (K / 2) + (ln >> 5) * (uint32_t)(MODE == 0 ? fd / 32 : K) + (ln & 15) * 4;
-    // Load i of 2 of the wave's part of token scale chunk c: rows 32 wave + 16 i .. + 15 (words past
-    // a row's end: its last).
-    auto issue_ts = [&](int c, int i) {
-      const int n = min(c * 4 + ((ln & 3) ^ ((2 * wave + i) & 3)), (ss >> 2) - 1);
-      g_load4(ascales, ots + i * ots_step + 4 * n, lds_ts + (c & 1) * (kGTsWords * 4) + (wave * 2 + i) * 256);
+    // Load i of 16 of token scale chunk c: rows 8 i .. 8 i + 7 (words past a row's end: its last).
+    auto ts_row = [&](int i) { return s_row[i * 8 + (ln >> 3)]; };
+    auto issue_ts = [&](int c, int i, uint32_t row) {
+      const int n = min(c * 8 + ((ln & 7) ^ (i & 7)), (ss >> 2) - 1);
+      g_load4(ascales, row + 4 * n, lds_ts + (c & 1) * (kGTsWords * 4) + i * 256);
     };
-    // The stage at LDS byte st <- step kt0 (at most nk - 1), and a load of the chunk that begins
-    // two to five steps later (each of its loads is issued twice): the eight loads, two a quarter.
-    auto issue = [&](uint32_t st, int kt0, auto quarter_tag) {
-      constexpr int qt = decltype(quarter_tag)::value;
+    // Stage kt0 mod 2 <- step kt0 (at most nk - 1), and load 2 (kt - 1) mod 16 + wave / 2 of the chunk after
+    // the one that step kt - 1 is in; `row` from ts_row(ts_load(kt)).
+    auto ts_load = [&](int kt) { return ((kt - 1) & 7) * 2 + (wave >> 1); };
+    auto issue = [&](int kt0, uint32_t row, auto h_tag) {
+      constexpr int hh = decltype(h_tag)::value;
       const int kt = min(kt0, nk - 1);
+      const uint32_t st = lds_sm + (kt0 & 1) * kGStage;
       const bool sh = half && kt == nk - 1;
-      if constexpr (qt < 2) {
-#pragma unroll
-        for (int t = 2 * qt; t < 2 * qt + 2; ++t)
-          g_load16(acodes, min(oa[t] + (uint32_t)kt * 128, last_piece), st + kGTokAt + (4 * wave + t) * 1024);
-      } else if constexpr (qt == 2) {
-        const uint32_t oc = (sh ? ln & 31 : ln) * 16;
-#pragma unroll
-        for (int s = 0; s < 2; ++s)
-          g_load16(wcodes + (size_t)kt * 1024 + s * strip, oc, st + kGCodeAt + (wave * 2 + s) * 1024);
-      } else {
-        g_load4(wscales + (size_t)kt * 64, ows - (sh ? (ln & 8) * 4 : 0), st + wn * 256);
-        issue_ts((kt0 + 2) >> 2, kt0 & 1);
+      const uint32_t oc = (sh ? ln & 31 : ln) * 16, osc = ows - (sh ? (ln & 8) * 4 : 0);
+      const uint8_t* const c0 = wcodes + (size_t)kt * 1024;
+      if (hh == 0) {
+        issue_ts(((kt0 - 1) >> 3) + 1, ts_load(kt0), row);
+        g_load4(wscales + (size_t)kt * 64, osc, st + wave * 256);
       }
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+        if (hh == t / 2)
+        g_load16(acodes, min(oa[t] + (uint32_t)kt * 128, last_piece), st + kGTokAt + (4 * wave + t) * 1024);
+#pragma unroll
+      for (int s = 0; s < 4; ++s)
+        if (hh == s / 2)
+        g_load16(c0 + (s & 1) * strip + (s >> 1) * second, oc, st + kGCodeAt + (wave * 4 + s) * 1024);
     };
-    using I0 = std::integral_constant<int, 0>;
-    using I1 = std::integral_constant<int, 1>;
-    using I2 = std::integral_constant<int, 2>;
-    using I3 = std::integral_constant<int, 3>;
+    using H0 = std::integral_constant<int, 0>;
+    using H1 = std::integral_constant<int, 1>;
 
-    // lane addresses of the operands (within a stage): token pieces by half step and piece, codes,
-    // scales; token tile it of the wave is rows 64 it + 32 wm .. + 31
+    // lane addresses of the operands: token pieces by half step and piece, codes, scales
     const int g = ln >> 5, i32 = ln & 31;
     uint32_t at_tok[2][2];
 #pragma unroll
     for (int kh = 0; kh < 2; ++kh)
 #pragma unroll
-      for (int c = 0; c < 2; ++c) at_tok[kh][c] = kGTokAt + (wm * 32 + i32) * 128 + ((4 * kh + 2 * c + g) ^ ((i32 >> 1) & 7)) * 16;
-    const uint32_t at_code = kGCodeAt + wn * 4096 + (i32 >> 4) * 1024 + g * 256 + (i32 & 15) * 16;
-    const uint32_t at_ws = wn * 256 + (i32 >> 4) * 64 + g * 16 + (i32 & 15);
-    const uint32_t at_ts = lds_ts + (wm * 32 + i32) * 16, x_ts = ((2 * wm + (i32 >> 4)) & 3) * 4;
+      for (int c = 0; c < 2; ++c) at_tok[kh][c] = lds_sm + kGTokAt + i32 * 128 + ((4 * kh + 2 * c + g) ^ ((i32 >> 1) & 7)) * 16;
+    const uint32_t at_code = lds_sm + kGCodeAt + wave * 4096 + (i32 >> 4) * 1024 + g * 256 + (i32 & 15) * 16;
+    const uint32_t at_ws = lds_sm + wave * 256 + (i32 >> 4) * 64 + g * 16 + (i32 & 15);
+    const uint32_t at_ts = lds_ts + i32 * 32, x_ts = (i32 >> 3) * 4;
 
     f32x16 acc[2][4];
 #pragma unroll
@@ -238,23 +280,19 @@ void m8_tile(FfnArgs p, const uint8_t* ascales, uint32_t last_piece, uint8_t* hs
       u32x4 w[2];
       uint32_t s[2];
     };
-    __syncthreads();  // the previous item's readers of the LDS are done
-    issue_ts(0, 0);
-    issue_ts(0, 1);
+    if (tid < kGM) s_row[tid] = row_at(min(tid, rows - 1)) * (uint32_t)ss;
+    __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      issue(lds_sm + i * kGStage, i, I0{});
-      issue(lds_sm + i * kGStage, i, I1{});
-      issue(lds_sm + i * kGStage, i, I2{});
-      issue(lds_sm + i * kGStage, i, I3{});
-    }
+    for (int i = 0; i < 4; ++i) issue_ts(0, wave * 4 + i, ts_row(wave * 4 + i));
+    issue(0, ts_row(ts_load(0)), H0{}); issue(0, 0, H1{});
     // AM token tiles in NP pairs; a step has NQ = 2 NP parts, part q = pair q % NP of half q / NP
     auto run_k = [&](auto am_tag) {
       constexpr int AM = decltype(am_tag)::value, NP = (AM + 1) / 2, NQ = 2 * NP;
       Tokens tk[2];
       Weights wt[2];
-      auto read = [&](uint32_t st, int kt, auto q_tag) {
+      auto read = [&](int kt, auto q_tag) {
         constexpr int q = decltype(q_tag)::value, kh = q / NP, pr = q % NP;
+        const uint32_t st = (kt & 1) * kGStage;
         if (pr == 0) {
 #pragma unroll
           for (int jn = 0; jn < 2; ++jn) {
@@ -262,14 +300,15 @@ void m8_tile(FfnArgs p, const uint8_t* ascales, uint32_t last_piece, uint8_t* hs
             wt[kh].s[jn] = g_lds<uint8_t>(at_ws + st, jn * 128 + kh * 32);
           }
         }
-        // word of row r, step n of the chunk: n ^ (r / 16) mod 4, r = 64 it + 32 wm + i32
-        const uint32_t ts = at_ts + ((kt >> 2) & 1) * (kGTsWords * 4) + (((kt & 3) * 4) ^ x_ts);
+        // word of row r, step n of the chunk: n ^ (r / 8) mod 8, r = 32 it + i32
+        const uint32_t ts = at_ts + ((kt >> 3) & 1) * (kGTsWords * 4) + (((kt & 7) * 4) ^ x_ts);
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          if (2 * pr + u >= AM) continue;
-          tk[q & 1].t[u][0] = g_lds<u32x4>(at_tok[kh][0] + st, (2 * pr + u) * 8192);
-          tk[q & 1].t[u][1] = g_lds<u32x4>(at_tok[kh][1] + st, (2 * pr + u) * 8192);
-          tk[q & 1].s[u] = g_lds<uint32_t>(ts, (2 * pr + u) * 1024);
+          constexpr int it0 = 2 * pr;
+          if (it0 + u >= AM) continue;
+          tk[q & 1].t[u][0] = g_lds<u32x4>(at_tok[kh][0] + st, (it0 + u) * 4096);
+          tk[q & 1].t[u][1] = g_lds<u32x4>(at_tok[kh][1] + st, (it0 + u) * 4096);
+          tk[q & 1].s[u] = g_lds<uint32_t>(ts ^ (u * 16), (it0 + u) * 1024);
         }
       };
       // The second half of a last step that has none: zeros (what was read may stand for NaN).
@@ -301,75 +340,56 @@ void m8_tile(FfnArgs p, const uint8_t* ascales, uint32_t last_piece, uint8_t* hs
       };
       using Q0 = std::integral_constant<int, 0>;
       using QL = std::integral_constant<int, NQ - 1>;
-      // Part q's products over the reads of part q + 1, `loads` issued between.
-      auto part = [&](uint32_t st, int kt, auto q_tag, auto loads) {
+      auto part = [&](int kt, auto q_tag, auto loads) {
         constexpr int q = decltype(q_tag)::value;
-        read(st, kt, std::integral_constant<int, (q + 1) % NQ>{});
+        read(kt, std::integral_constant<int, (q + 1) % NQ>{});
         __builtin_amdgcn_sched_barrier(0);
         loads();
         multiply(q_tag);
         __builtin_amdgcn_sched_barrier(0);
       };
-      using QL = std::integral_constant<int, NQ - 1>;
       using Q1 = std::integral_constant<int, 1 % NQ>;
       using Q2 = std::integral_constant<int, (NQ + 2) % NQ>;
-      uint32_t st = lds_sm, st1 = lds_sm + kGStage, st2 = lds_sm + 2 * kGStage;
-      issue(st2, 2, I0{});
-      if constexpr (NQ == 2) issue(st2, 2, I1{});
-      g_wait_loads<kGLoads + 8 / NQ>();
-      lds_barrier();
-      read(st, 0, Q0{});
-      // A step: every part's operands are read under the products of the part before; ahead of
-      // the last part's products the next step's stage is complete and this one's read by every
-      // wave, and from there on to the same place of the next step the loads of the third step from
-      // here go out (past the end: the last step's again, never read), some in each part: all at
-      // once they hold a wave up until the address unit has taken them.
-      for (int kt = 0; kt + 1 < nk; ++kt) {
-        if constexpr (NQ == 4) {
-          part(st, kt, Q0{}, [&] { issue(st2, kt + 2, I1{}); });
-          part(st, kt, Q1{}, [&] { issue(st2, kt + 2, I2{}); });
-          part(st, kt, Q2{}, [&] { issue(st2, kt + 2, I3{}); });
-        } else {
-          part(st, kt, Q0{}, [&] {
-            issue(st2, kt + 2, I2{});
-            issue(st2, kt + 2, I3{});
-          });
-        }
-        g_wait_loads<kGLoads>();
-        lds_barrier();
-        part(st1, kt + 1, QL{}, [&] {
-          issue(st, kt + 3, I0{});
-          if constexpr (NQ == 2) issue(st, kt + 3, I1{});
-        });
-        const uint32_t t = st;
-        st = st1;
-        st1 = st2;
-        st2 = t;
-      }
       auto none = [] {};
-      part(st, nk - 1, Q0{}, none);
+      g_wait_loads<0>();
+      lds_barrier();
+      issue(1, ts_row(ts_load(1)), H0{});
+      read(0, Q0{});
+      for (int kt = 0; kt + 1 < nk; ++kt) {
+        const uint32_t row = ts_row(ts_load(kt + 2));
+        part(kt, Q0{}, [&] { issue(kt + 1, row, H1{}); });
+        if constexpr (NQ == 4) {
+          part(kt, Q1{}, none);
+          part(kt, Q2{}, none);
+        }
+        g_wait_loads<0>();
+        lds_barrier();
+        part(kt + 1, QL{}, [&] { issue(kt + 2, row, H0{}); });
+      }
+      part(nk - 1, Q0{}, none);
       blank(Q1{});
       if constexpr (NQ == 4) {
-        part(st, nk - 1, Q1{}, none);
+        part(nk - 1, Q1{}, none);
         blank(Q2{});
-        part(st, nk - 1, Q2{}, none);
+        part(nk - 1, Q2{}, none);
         blank(QL{});
       }
       multiply(QL{});
       g_wait_loads<0>();  // those past the end too: the next item's may not be overtaken
     };
-    switch ((rows + 63) >> 6) {
+    switch ((rows + 31) >> 5) {
       case 1: run_k(std::integral_constant<int, 1>{}); break;
       case 2: run_k(std::integral_constant<int, 2>{}); break;
       case 3: run_k(std::integral_constant<int, 3>{}); break;
       default: run_k(std::integral_constant<int, 4>{}); break;
     }
+    if (tid == 0) settle(next_q, next_j);
 
     // lane 32 g + i, value v: token row i, weight row 8 (v / 4) + 4 g + v % 4 of the tile's 32
 #pragma unroll
     for (int it = 0; it < 4; ++it) {
-      if (it * 64 + wm * 32 >= rows || !out) continue;
-      const int r = it * 64 + wm * 32 + i32;
+      if (it * 32 >= rows || !out) continue;
+      const int r = it * 32 + i32;
       if (MODE == 0) {
         const int u0 = r0;
         float h[16];
@@ -420,6 +440,7 @@ void m8_tile(FfnArgs p, const uint8_t* ascales, uint32_t last_piece, uint8_t* hs
         }
       }
     }
+    __syncthreads();  // the next item is there
   }
 }
 
@@ -430,16 +451,25 @@ bool ffn_mx8_gemm_supported(long long T, int k, int d, int f) {
   return T * d <= (1ll << 32) && T * k * f <= (1ll << 32);
 }
 
+size_t ffn_mx8_plan_bytes(long long A, int E) {
+  return 4 * kPlanTiles + sizeof(PlanTile) * (size_t)(A / kGM + std::min<long long>(A, E));
+}
+
 int launch_ffn_mx8_gemm(const FfnArgs& p, int T, int y_dtype, hipStream_t stream) {
   const uint8_t* xs = (const uint8_t*)p.x + (size_t)T * p.d;
-  uint8_t* hs = (uint8_t*)p.h + (size_t)T * p.k * p.f;
-  const dim3 grid((num_cus() + 7) / 8 * 8), blk(512);
+  const size_t A = (size_t)T * p.k;
+  uint8_t* hs = (uint8_t*)p.h + A * p.f;
+  int* plan = (int*)(hs + (A * mxfp8_scale_stride(p.f) + 255) / 256 * 256);
+  // two workgroups a CU: the hand-off of a stage in one is covered by the other's products
+  const dim3 grid((num_cus() * 2 + 7) / 8 * 8), blk(256);
   const int ntd = (p.d + 255) / 256;
-  const uint32_t last_h = (uint32_t)((size_t)T * p.k * p.f - 16);
-  hipLaunchKernelGGL((m8_tile<0, MOE_BF16>), grid, blk, 0, stream, p, xs, (uint32_t)((size_t)T * p.d - 16), hs, (p.f + 127) / 128);
+  const uint32_t last_x = (uint32_t)((size_t)T * p.d - 16), last_h = (uint32_t)(A * p.f - 16);
+  hipLaunchKernelGGL(m8_plan, dim3(1), dim3(kMaxE), 0, stream, p, plan);
   MOE_LAUNCH_CHECK();
-  if (y_dtype == MOE_F32) hipLaunchKernelGGL((m8_tile<1, MOE_F32>), grid, blk, 0, stream, p, hs, last_h, nullptr, ntd);
-  else hipLaunchKernelGGL((m8_tile<1, MOE_BF16>), grid, blk, 0, stream, p, hs, last_h, nullptr, ntd);
+  hipLaunchKernelGGL((m8_tile<0, MOE_BF16>), grid, blk, 0, stream, p, xs, last_x, hs, (p.f + 127) / 128, plan);
+  MOE_LAUNCH_CHECK();
+  if (y_dtype == MOE_F32) hipLaunchKernelGGL((m8_tile<1, MOE_F32>), grid, blk, 0, stream, p, hs, last_h, nullptr, ntd, plan);
+  else hipLaunchKernelGGL((m8_tile<1, MOE_BF16>), grid, blk, 0, stream, p, hs, last_h, nullptr, ntd, plan);
   MOE_LAUNCH_CHECK();
   return MOE_OK;
 }

@@ -200,7 +200,8 @@ int moe_rmsnorm(const void* x, int x_dtype, const void* delta, int delta_dtype, 
                 void* y8, hipStream_t stream);
 
 /* Workspace bytes for moe_expert_ffn: the SwiGLU intermediate [T*k][f] (2 bytes per unit,
- * 4 with MOE_F32 activations; with MOE_MXFP8 activations T*k MXFP8 rows of f units), and up to 16 tokens with MOE_BF16 activations 4 bytes per
+ * 4 with MOE_F32 activations; with MOE_MXFP8 activations T*k MXFP8 rows of f units and a
+ * work list), and up to 16 tokens with MOE_BF16 activations 4 bytes per
  * unit, room for the one-launch MXFP4 path (see moe_expert_ffn's ws). */
 size_t moe_expert_ffn_workspace_bytes(int T, int k, int f, int act_dtype);
 
@@ -235,7 +236,7 @@ size_t moe_expert_ffn_workspace_bytes(int T, int k, int f, int act_dtype);
  *  key_base + e, or a negative slot, sets *status = MOE_ERANGE and that
  *  expert's rows are not written (stale-cache detection).
  *  ws: 16-byte aligned, at least T*k*f*2 bytes (4 with MOE_F32 activations,
- *  moe_mxfp8_bytes(T*k, f) with MOE_MXFP8), or MOE_EINVAL.  With MOE_MXFP4 weights and MOE_BF16 activations on the weight-streaming path, T <= 16,
+ *  moe_expert_ffn_workspace_bytes(T, k, f, MOE_MXFP8) with MOE_MXFP8), or MOE_EINVAL.  With MOE_MXFP4 weights and MOE_BF16 activations on the weight-streaming path, T <= 16,
  *  min(E, T*k)*f >= 65536 and at least T*k*f*4 bytes (what
  *  moe_expert_ffn_workspace_bytes returns there), both projections run in one launch that
  *  exchanges h through tagged entries in ws (zeroed by a small kernel first); the results
@@ -256,7 +257,7 @@ int moe_expert_ffn(const void* x, int act_dtype, const int32_t* perm, const int3
  * up that device's array address once).  Every other argument, result and error is as for
  * moe_expert_ffn, which it calls with the array as ws (so calls of up to 16 tokens whose
  * tagged entries fit take the one-launch MXFP4 path).  A call whose intermediate (T*k*f*2
- * bytes, 4 with MOE_F32 activations, T*k MXFP8 rows with MOE_MXFP8) exceeds the array returns MOE_ETOOBIG before anything
+ * bytes, 4 with MOE_F32 activations, the whole workspace with MOE_MXFP8) exceeds the array returns MOE_ETOOBIG before anything
  * is enqueued.  All calls on
  * one GPU share its array and each overwrites it: calls that may overlap in time on one GPU
  * (different streams, or different host threads) race and give undefined results; order them

@@ -295,7 +295,7 @@ def _ffn(w, x8, perm, offsets, arena, stride, ydt=moe.MOE_F32, path=moe.MOE_PATH
         moe.moe_expert_ffn_noalloc(x8, moe.MOE_MXFP8, perm, offsets, w.T, w.k, w.E, w.d, w.f, slots, arena, stride,
                                    moe.MOE_MXFP4, mask, keys, 0, y, ydt, path, status, stream)
     else:
-        nws = moe.moe_mxfp8_bytes(A, w.f)
+        nws = moe.moe_expert_ffn_workspace_bytes(w.T, w.k, w.f, moe.MOE_MXFP8)
         ws = _bytes(nws + 256)
         moe.moe_expert_ffn(x8, moe.MOE_MXFP8, perm, offsets, w.T, w.k, w.E, w.d, w.f, slots, arena, stride,
                            moe.MOE_MXFP4, mask, keys, 0, ws, nws, y, ydt, path, status, stream)
@@ -572,7 +572,7 @@ def test_two_layers_side_by_side_on_two_streams():
     want = [_ffn(w, c[1], dev(c[2]), dev(c[3]), arena, w.entry_bytes)[0] for c in cases]
     args = [(c[1], dev(c[2]), dev(c[3])) for c in cases]
     A = w.T * w.k
-    ws = [_bytes(moe.moe_mxfp8_bytes(A, w.f)) for _ in cases]
+    ws = [_bytes(moe.moe_expert_ffn_workspace_bytes(w.T, w.k, w.f, moe.MOE_MXFP8)) for _ in cases]
     y = [torch.zeros((A, w.d), device="cuda") for _ in cases]
     streams = [torch.cuda.Stream() for _ in cases]
     torch.cuda.synchronize()

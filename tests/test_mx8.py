@@ -134,7 +134,7 @@ def test_entry_conversions_refuse(change, want):
 def test_expert_ffn_with_mxfp8_activations_refuses():
     eb = moe.moe_entry_bytes(4096, 2048, X4)
     base = [A, X8, A, A, 8, 6, 256, 4096, 2048, None, A, eb, X4, None, None, 0, A,
-            moe.moe_mxfp8_bytes(48, 2048), A, F32, 0, None, None]
+            moe.moe_expert_ffn_workspace_bytes(8, 6, 2048, X8), A, F32, 0, None, None]
 
     def rc(**kw):
         a = list(base)
@@ -144,7 +144,7 @@ def test_expert_ffn_with_mxfp8_activations_refuses():
     assert rc(_12=BF16, _11=3 * 4096 * 2048 * 2) == EUNSUP  # MXFP4 weights only
     assert rc(_12=F32, _11=3 * 4096 * 2048 * 4) == EUNSUP
     assert rc(_19=X8) == EUNSUP and rc(_19=X4) == EUNSUP     # y in fp32 or bf16
-    assert rc(_17=base[17] - 1) == EINVAL                    # workspace below T*k MXFP8 rows
+    assert rc(_17=base[17] - 256) == EINVAL                  # a short workspace
     assert rc(_11=eb - 16) == EINVAL and rc(_7=4000) == EINVAL and rc(_0=None) == EINVAL
     assert rc(_0=A + 8) == EINVAL and rc(_20=3) == EINVAL
     assert rc(_4=0) == 0
