@@ -86,17 +86,20 @@ struct PlanTile {
 };
 __host__ __device__ constexpr int plan_counter(int mode, int xcd) { return 16 * (8 * mode + xcd); }
 
-// One workgroup.  Shares are cut by cost, a tile's being its 32-row products and two for what an
-// item costs beside them.
+// One workgroup: tiles and costs per expert and their prefixes (a thread an expert), then the
+// tiles (a thread a tile).  Shares are cut by cost, a tile's being its 32-row products and two for
+// what an item costs beside them.
+__device__ __forceinline__ int plan_cost(int rows) { return (rows + 31) / 32 + 2; }
+
 __global__ __launch_bounds__(kMaxE) void m8_plan(FfnArgs p, int* plan) {
+  __shared__ int s_first[kMaxE + 1];
+  __shared__ long long s_before[kMaxE];
   __shared__ int s_cnt[kMaxE / 64];
   __shared__ long long s_cost[kMaxE / 64];
   const int e = threadIdx.x, lane = e & 63, wave = e >> 6;
-  const int n0 = e < p.E && active(p, e) ? p.offsets[e] : 0;
-  const int n = e < p.E && active(p, e) ? p.offsets[e + 1] - n0 : 0;
+  const int n = e < p.E && active(p, e) ? p.offsets[e + 1] - p.offsets[e] : 0;
   const int tiles = (n + kGM - 1) / kGM;
-  auto cost_of = [](int rows) { return (rows + 31) / 32 + 2; };
-  const long long cost = tiles ? (long long)(tiles - 1) * cost_of(kGM) + cost_of(n - (tiles - 1) * kGM) : 0;
+  const long long cost = tiles ? (long long)(tiles - 1) * plan_cost(kGM) + plan_cost(n - (tiles - 1) * kGM) : 0;
   int x = tiles;
   long long y = cost;
 #pragma unroll
@@ -116,6 +119,7 @@ __global__ __launch_bounds__(kMaxE) void m8_plan(FfnArgs p, int* plan) {
   __syncthreads();
   int first = x - tiles, all = 0;
   long long before = y - cost, total = 0;
+#pragma unroll
   for (int w = 0; w < kMaxE / 64; ++w) {
     if (w < wave) {
       first += s_cnt[w];
@@ -124,17 +128,25 @@ __global__ __launch_bounds__(kMaxE) void m8_plan(FfnArgs p, int* plan) {
     all += s_cnt[w];
     total += s_cost[w];
   }
+  s_first[e] = first;
+  s_before[e] = before;
+  if (e == 0) s_first[kMaxE] = all;
   if (e <= 8) plan[kPlanShares + e] = e == 0 ? 0 : all;
   __syncthreads();
-  PlanTile* t = (PlanTile*)(plan + kPlanTiles);
-  for (int m = 0; m < tiles; ++m) {
-    const int rows = min(kGM, n - m * kGM);
-    t[first + m] = PlanTile{e, n0 + m * kGM, rows, 0};
+  for (int m = threadIdx.x; m < all; m += kMaxE) {
+    int lo = 0, hi = kMaxE;  // the last expert whose first tile is not past m
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (s_first[mid] <= m) lo = mid; else hi = mid;
+    }
+    const int i = m - s_first[lo], n0 = p.offsets[lo] + i * kGM;
+    const int rows = min(kGM, p.offsets[lo + 1] - n0);
+    ((PlanTile*)(plan + kPlanTiles))[m] = PlanTile{lo, n0, rows, 0};
+    const long long at = s_before[lo] + (long long)i * plan_cost(kGM);
     for (int c = 1; c < 8; ++c) {  // the share that begins in this tile's cost begins with it
       const long long cut = total * c / 8;
-      if (cut >= before && cut < before + cost_of(rows)) plan[kPlanShares + c] = first + m;
+      if (cut >= at && cut < at + plan_cost(rows)) plan[kPlanShares + c] = m;
     }
-    before += cost_of(rows);
   }
 }
 
