@@ -42,7 +42,13 @@ constexpr int kMxMaxRows = 16;
 // (T*k / E), MXFP4 experts above kMxGemmMinRowsPerExpert (their streaming path, with the row
 // split above, stays ahead to about 5 rows per expert at Zipf 0.2 and beyond 8 when skewed).
 constexpr long long kGemmMinRowsPerExpert = 2, kMxGemmMinRowsPerExpert = 8;
+// MXFP8 activations: the grouped GEMM above 4 rows per expert on average, weight streaming for
+// every expert up to 32 tokens, split by rows at kMxMaxRows between.  d = 4096, f = 2048, top 6 of
+// 256, Zipf 0.2 / 1, streaming | split | GEMM in us: T = 24 223 / 95 | 232 / 119 | 278 / 82; T = 64
+// 371 / 171 | 381 / 134 | 424 / 133; T = 128 477 / 344 | 525 / 172 | 545 / 149; T = 256 551 / 597 |
+// 598 / 195 | 582 / 192.
 constexpr long long kMx8GemmMinRowsPerExpert = 4;
+constexpr int kMx8MaxT = 32;
 // Rounds of resident workgroups in the row-split dot-product launches (each loops over items).
 constexpr int kDotSplitRounds = 2;
 
@@ -159,11 +165,17 @@ extern "C" int moe_expert_ffn(const void* x, int act_dtype, const int32_t* perm,
     MOE_LAUNCH_CHECK();
     return MOE_OK;
   }
-  if (act_dtype == MOE_MXFP8) {
-    if (path == MOE_PATH_AUTO)
-      path = (long long)T * k <= kMx8GemmMinRowsPerExpert * E || !mx8_gemm_fits ? MOE_PATH_GEMV : MOE_PATH_GEMM;
-    if (path == MOE_PATH_GEMM) return launch_ffn_mx8_gemm(p, T, y_dtype, stream);
-    return launch_ffn_mx8(p, T, y_dtype, stream, std::min(E, T * k));
+  if (act_dtype == MOE_MXFP8) {  // as below, with kernels and thresholds of its own
+    const int A = T * k, experts = std::min(E, A);
+    const bool gemm = path == MOE_PATH_GEMM || (path == MOE_PATH_AUTO && (long long)T * k > kMx8GemmMinRowsPerExpert * E);
+    if (gemm && mx8_gemm_fits) return launch_ffn_mx8_gemm(p, T, y_dtype, stream);
+    if (path == MOE_PATH_GEMV || T <= kMx8MaxT || !mx8_gemm_fits) return launch_ffn_mx8(p, T, y_dtype, stream, experts);
+    FfnArgs few = p, many = p;
+    few.nmax = kMxMaxRows;
+    many.nmin = kMxMaxRows + 1;
+    int rc = launch_ffn_mx8(few, T, y_dtype, stream, experts);
+    if (rc == MOE_OK) rc = launch_ffn_mx8_gemm(many, T, y_dtype, stream);
+    return rc;
   }
   if (mx) {
     const bool gemm = path == MOE_PATH_GEMM ||

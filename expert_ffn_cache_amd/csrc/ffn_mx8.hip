@@ -28,7 +28,7 @@
 namespace moe {
 namespace {
 
-constexpr int kM8Ahead = 4;              // weight tiles in flight per wave and matrix
+constexpr int kM8Ahead = 2;              // weight tiles in flight per wave and matrix
 constexpr int kM8Codes = 32768;          // LDS bytes of staged codes
 constexpr int kM8Pad = 16;               // bytes between staged rows (bank spread)
 
@@ -110,6 +110,26 @@ __device__ __forceinline__ void m8_tile_mma(const MxTile<NMAT>& t, const uint8_t
                                                               (int)t.s[m], 0, (int)xs);
 }
 
+// Partial sums of the KS waves of each strip pair, through the staged rows' LDS: waves ks > 0
+// store, then the first wave adds.
+template <int NMAT, int KS>
+__device__ __forceinline__ void m8_reduce(M8Lds& lds, f32x4 (&acc)[NMAT], int pr, int ks, int lane) {
+  if (KS == 1) return;
+  f32x4* red = (f32x4*)lds.codes;  // [3][NMAT][64]
+  __syncthreads();  // the staged rows are read
+  if (ks > 0) {
+#pragma unroll
+    for (int m = 0; m < NMAT; ++m) red[((pr * (KS - 1) + ks - 1) * NMAT + m) * 64 + lane] = acc[m];
+  }
+  __syncthreads();
+  if (ks == 0) {
+#pragma unroll
+    for (int j = 1; j < KS; ++j)
+#pragma unroll
+      for (int m = 0; m < NMAT; ++m) acc[m] += red[((pr * (KS - 1) + j - 1) * NMAT + m) * 64 + lane];
+  }
+}
+
 // The wave's share of all K for one block of up to 16 rows: acc[m] (+)= strip m x rows.
 template <int NMAT, int KS, typename RowOf>
 __device__ __forceinline__ void m8_rows(M8Lds& lds, const uint8_t* codes, const uint8_t* scales,
@@ -169,7 +189,7 @@ __device__ __forceinline__ void m8_store_h(uint8_t* codes, uint8_t* scale, int l
 
 // Gate/up: workgroup = 4/KS pairs of strips (32 units each) of one expert.
 template <int KS>
-__global__ __launch_bounds__(256) void m8_gateup(FfnArgs p, const uint8_t* xs, uint8_t* hs) {
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4))) void m8_gateup(FfnArgs p, const uint8_t* xs, uint8_t* hs) {
   __shared__ __attribute__((aligned(16))) M8Lds lds;
   constexpr int TR = 4 / KS;
   const int npair = p.f >> 5, nb = (npair + TR - 1) / TR;
@@ -192,7 +212,7 @@ __global__ __launch_bounds__(256) void m8_gateup(FfnArgs p, const uint8_t* xs, u
     f32x4 acc[4];
     m8_rows<4, KS>(lds, (const uint8_t*)p.x, xs, K, nt, [&](int t) { return p.perm[n0 + m0 + t] / p.k; }, cb, sb,
                    ks, lane, work, acc);
-    mx_reduce<4, KS>(acc, pr, ks, lane);
+    m8_reduce<4, KS>(lds, acc, pr, ks, lane);
     if (ks == 0 && work) {
       float h[8];
 #pragma unroll
@@ -229,7 +249,7 @@ __global__ __launch_bounds__(256) void m8_down(FfnArgs p, const uint8_t* hs) {
     const int nt = min(16, n - m0);
     f32x4 acc[2];
     m8_rows<2, KS>(lds, (const uint8_t*)p.h, hs, K, nt, [&](int t) { return n0 + m0 + t; }, cb, sb, ks, lane, work, acc);
-    mx_reduce<2, KS>(acc, pr, ks, lane);
+    m8_reduce<2, KS>(lds, acc, pr, ks, lane);
     const int t = lane & 15, g = lane >> 4;
     if (ks == 0 && work && t < nt) {
       const size_t o = (size_t)(n0 + m0 + t) * p.d + 32 * pair + 4 * g;

@@ -168,43 +168,61 @@ void m8_tile(FfnArgs p, const uint8_t* ascales, uint32_t last_piece, uint8_t* hs
   const uint8_t* acodes = (const uint8_t*)(MODE == 0 ? p.x : p.h);
 
   // Items of this XCD's share first, then of the others', so no workgroup stops early; a share's
-  // queue runs over its token tiles, four of them to a weight tile.  Thread 0 draws the next item
-  // while the current one is computed.
+  // queue runs over its token tiles, four of them to a weight tile.  The next item is drawn while
+  // the current one is computed.
   const int* const share = plan + kPlanShares;
   const PlanTile* const tiles = (const PlanTile*)(plan + kPlanTiles);
-  auto draw = [&](int q) { return atomicAdd(plan + plan_counter(MODE, q & 7), 1); };
-  auto settle = [&](int q, int j) {  // item j of share q if there is one, else of the next share that has
-    const int q0 = blockIdx.x & 7;
-    while (j >= (share[(q & 7) + 1] - share[q & 7]) * n_ntiles) {
-      if (++q >= q0 + 8) {
-        q = -1;
-        break;
+  auto share_items = [&](int q) { return (share[q + 1] - share[q]) * n_ntiles; };
+  auto draw = [&](int q) { return atomicAdd(plan + plan_counter(MODE, q), 1); };
+  // Called by wave 0: item j of share q if there is one, else the next of the nearest share that
+  // has one left (all eight counters are looked at together).
+  auto settle = [&](int q, int j) {
+    if (j >= share_items(q)) {
+      const int c = ((int)blockIdx.x + lane) & 7, n = share_items(c);
+      for (;;) {
+        const bool left = lane < 8 && n > 0 &&
+            __hip_atomic_load(plan + plan_counter(MODE, c), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) < n;
+        const unsigned long long m = __ballot(left);
+        if (!m) {
+          q = -1;
+          break;
+        }
+        const int l = __ffsll((long long)m) - 1;
+        q = ((int)blockIdx.x + l) & 7;
+        j = 0;
+        if (lane == 0) j = draw(q);
+        j = __shfl(j, 0);
+        if (j < share_items(q)) break;
       }
-      j = draw(q);
     }
-    s_item[0] = q;
-    s_item[1] = j;
+    if (lane == 0) {
+      s_item[0] = q;
+      s_item[1] = j;
+    }
   };
+  // drawn ahead: held by lane 0 of wave 0
   int next_q = blockIdx.x & 7, next_j = 0;
-  if (tid == 0) settle(next_q, draw(next_q));
+  if (wave == 0) {
+    const int n = share_items(next_q);
+    if (lane == 0) next_j = n > 0 ? draw(next_q) : 0;
+    settle(next_q, __shfl(next_j, 0));
+  }
   __syncthreads();
 
   for (;;) {
     const int q = s_item[0], j = s_item[1];
     if (q < 0) return;
-    const int m_0 = share[q & 7], m_n = share[(q & 7) + 1] - m_0;
+    const int m_0 = share[q], m_n = share[q + 1] - m_0;
     const int grp = j / (4 * n_ntiles), gsz = min(4, m_n - grp * 4), in = j - grp * 4 * n_ntiles;
     const int nt = in / gsz;
     const PlanTile tile = tiles[m_0 + grp * 4 + (in - nt * gsz)];
     const int n0 = tile.n0, rows = tile.rows;
     const uint8_t* W = (const uint8_t*)entry_of(p, tile.e);
     __syncthreads();  // the item is read, and the previous one's readers of the LDS are done
-    if (tid == 0) {
-      next_q = q;
-      next_j = draw(q);
-    }
+    next_q = q;
+    if (tid == 0) next_j = draw(q);
     if (!W) {
-      if (tid == 0) settle(next_q, next_j);
+      if (wave == 0) settle(next_q, __shfl(next_j, 0));
       __syncthreads();
       continue;
     }
@@ -395,7 +413,7 @@ void m8_tile(FfnArgs p, const uint8_t* ascales, uint32_t last_piece, uint8_t* hs
       case 3: run_k(std::integral_constant<int, 3>{}); break;
       default: run_k(std::integral_constant<int, 4>{}); break;
     }
-    if (tid == 0) settle(next_q, next_j);
+    if (wave == 0) settle(next_q, __shfl(next_j, 0));
 
     // lane 32 g + i, value v: token row i, weight row 8 (v / 4) + 4 g + v % 4 of the tile's 32
 #pragma unroll
