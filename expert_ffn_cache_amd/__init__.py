@@ -136,10 +136,22 @@ def _p(x):
     return x.data_ptr()
 
 
+_current_stream = None  # () -> torch's current hipStream_t on the current device
+
+
 def _s(stream):
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        global _current_stream
+        if _current_stream is None:
+            import torch
+            # 0.3 us against 2.7 us through a torch.cuda.Stream object, of 7 us for a whole call
+            raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+            device = torch.cuda.current_device
+            if raw is None:
+                _current_stream = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
+            else:
+                _current_stream = lambda: raw(device())  # noqa: E731
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

@@ -6,10 +6,12 @@
 // v_cvt_scalef32_pk_fp4_{f32,bf16} does).  A block that holds an infinity or a NaN gets the
 // scale 255 and dequantises to NaN.
 //
-// Work split: a thread owns one block (64 bytes of bf16, 128 of fp32; 16 code bytes and a scale
-// byte).  Blocks are numbered as the MXFP4 entry stores them (inside a 16-row strip: block b of
-// all 16 rows, then block b + 1), so the code side is contiguous over a wave and the other side
-// covers 16 rows x 256 (512) bytes.  HBM-bound: 2.53 (4.53) bytes a weight.
+// Work split: a wave converts one tile of the entry layout at a time (16 rows x 128 elements, 64
+// elements in a row strip's last one where K is not a multiple of 128), a lane one block of it.
+// The code side of a tile is 1 KB in lane order; the plain side is 16 row pieces of 256 (fp32 512)
+// bytes, moved 16 lanes to a row piece and exchanged between lanes through LDS (the 16-byte
+// pieces of row i permuted by i, so neither side's accesses collide).  HBM-bound: 2.53 (4.53)
+// bytes a weight.
 #include <algorithm>
 
 #include "mx8_dev.h"
@@ -18,100 +20,162 @@ using namespace moe;
 
 namespace {
 
-// Block g of an entry (numbered over the three matrices in storage order): its first element
-// in the plain layout, its 16 code bytes and its scale byte in the MXFP4 layout.
-struct BlockAt {
+// Tile g of an entry's three matrices: where its codes, scales and plain rows start.
+struct TileAt {
   size_t elem, code, scale;
+  unsigned K, blocks;  // row length, blocks of a row in the tile (4, or 2 in a short last one)
 };
-__device__ __forceinline__ BlockAt block_at(unsigned g, unsigned per_mat, int d, int f) {
-  const unsigned m = g / per_mat, b = g - m * per_mat;  // matrix, block in the matrix
-  const unsigned K = m == 2 ? f : d, per_strip = K >> 1;  // 16 rows x K/32 blocks
-  const unsigned rt = b / per_strip, in = b - rt * per_strip;
-  const unsigned row = rt * 16 + (in & 15), kb = in >> 4;
-  return BlockAt{(size_t)m * d * f + (size_t)row * K + kb * 32, (size_t)g * 16,
-                 3 * ((size_t)d * f / 2) + g};
+__device__ __forceinline__ TileAt tile_at(unsigned g, int d, int f) {
+  const unsigned kd = (d + 127) >> 7, kf = (f + 127) >> 7, per_gu = (f >> 4) * kd;
+  const unsigned m = g < per_gu ? 0 : g < 2 * per_gu ? 1 : 2;
+  const unsigned in = g - m * per_gu, K = m == 2 ? f : d, nk = m == 2 ? kf : kd;
+  const unsigned rt = in / nk, kt = in - rt * nk;
+  const size_t fd = (size_t)d * f;
+  return TileAt{m * fd + (size_t)rt * 16 * K + kt * 128, m * (fd / 2) + (size_t)rt * 8 * K + (size_t)kt * 1024,
+                3 * (fd / 2) + m * (fd / 32) + (size_t)rt * (K / 2) + (size_t)kt * 64, K, min(4u, (K >> 5) - 4 * kt)};
+}
+__host__ __device__ inline size_t entry_tiles(int d, int f) {
+  return 2 * (size_t)(f >> 4) * ((d + 127) >> 7) + (size_t)(d >> 4) * ((f + 127) >> 7);
+}
+
+// The wave's LDS: 16 rows of PC 16-byte pieces, piece c of row i at c ^ i.  A tile with `blocks`
+// blocks a row uses the first blocks * PB pieces of a row.
+template <int DT>
+struct Pieces {
+  static constexpr int kElem = DT == MOE_F32 ? 4 : 2, PB = 2 * kElem, PC = 4 * PB;  // pieces of a block, of a row
+};
+// order between the lanes of a wave: its LDS operations are served in order
+__device__ __forceinline__ void wave_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
 template <int SDT>
 __global__ __launch_bounds__(256) void entry_quantize(const char* src, size_t src_stride, int d,
-                                                      int f, char* dst, size_t dst_stride) {
-  const unsigned per_mat = (unsigned)((size_t)d * f / 32);
+                                                      int f, char* dst, size_t dst_stride, unsigned ntiles) {
+  using P = Pieces<SDT>;
+  __shared__ u32x4 s_p[4][16 * P::PC];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  u32x4* const lp = s_p[wave];
   const char* se = src + blockIdx.y * src_stride;
   char* de = dst + blockIdx.y * dst_stride;
-  for (unsigned g = blockIdx.x * 256 + threadIdx.x; g < 3 * per_mat; g += gridDim.x * 256) {
-    const BlockAt at = block_at(g, per_mat, d, f);
-    u32x4 v[SDT == MOE_F32 ? 8 : 4];
-    const char* s = se + at.elem * (SDT == MOE_F32 ? 4 : 2);
+  for (unsigned g = blockIdx.x * 4 + wave; g < ntiles; g += gridDim.x * 4) {
+    const TileAt at = tile_at(g, d, f);
+    const int sh = (at.blocks == 4 ? 2 : 1) + (SDT == MOE_F32 ? 3 : 2);  // log2 of pieces a row
+    const char* s = se + at.elem * P::kElem;
+    const int passes = 16 << sh >> 6;
+    u32x4 v[P::PB];
 #pragma unroll
-    for (int i = 0; i < (SDT == MOE_F32 ? 8 : 4); ++i) v[i] = ldg16(s + 16 * i);
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < (SDT == MOE_F32 ? 8 : 4); ++i)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        if (SDT == MOE_F32) m = max(m, v[i][q] & 0x7FFFFFFFu);
-        else m = max(m, max(v[i][q] & 0x7FFF0000u, (v[i][q] << 16) & 0x7FFF0000u));
-      }
-    const int e = (int)(m >> 23);
-    const uint32_t sb = e == 255 ? 255u : (uint32_t)max(e - 2, 0);
-    u32x4 c{0u, 0u, 0u, 0u};
-    if (e != 255) {
-      const float sc = e8m0_value(sb);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint32_t w = 0;
-        if (SDT == MOE_F32) {
-          const f32x4 a = __builtin_bit_cast(f32x4, v[2 * i]), b = __builtin_bit_cast(f32x4, v[2 * i + 1]);
-          w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, a[0], a[1], sc, 0);
-          w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, a[2], a[3], sc, 1);
-          w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, b[0], b[1], sc, 2);
-          w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, b[2], b[3], sc, 3);
-        } else {
-          const uint32_t p0 = v[i][0], p1 = v[i][1], p2 = v[i][2], p3 = v[i][3];
-          w = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(w, __builtin_bit_cast(bf16x2, p0), sc, 0);
-          w = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(w, __builtin_bit_cast(bf16x2, p1), sc, 1);
-          w = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(w, __builtin_bit_cast(bf16x2, p2), sc, 2);
-          w = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(w, __builtin_bit_cast(bf16x2, p3), sc, 3);
-        }
-        c[i] = w;
-      }
+    for (int r = 0; r < P::PB; ++r) {  // 64 pieces a pass
+      const int id = r * 64 + lane, row = id >> sh, c = id & ((1 << sh) - 1);
+      if (r < passes) v[r] = ldg16_nt(s + ((size_t)row * at.K * P::kElem + c * 16));
     }
-    *(u32x4*)(de + at.code) = c;
-    de[at.scale] = (char)sb;
+    wave_fence();  // the previous tile's readers are done
+#pragma unroll
+    for (int r = 0; r < P::PB; ++r) {
+      const int id = r * 64 + lane, row = id >> sh, c = id & ((1 << sh) - 1);
+      if (r < passes) lp[row * P::PC + (c ^ row)] = v[r];
+    }
+    wave_fence();
+    const int i = lane & 15, q = lane >> 4;
+    if (q < (int)at.blocks) {
+      uint32_t m = 0;
+#pragma unroll
+      for (int c = 0; c < P::PB; ++c) {
+        v[c] = lp[i * P::PC + ((q * P::PB + c) ^ i)];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if (SDT == MOE_F32) m = max(m, v[c][e] & 0x7FFFFFFFu);
+          else m = max(m, max(v[c][e] & 0x7FFF0000u, (v[c][e] << 16) & 0x7FFF0000u));
+        }
+      }
+      const int e = (int)(m >> 23);
+      const uint32_t sb = e == 255 ? 255u : (uint32_t)max(e - 2, 0);
+      u32x4 code{0u, 0u, 0u, 0u};
+      if (e != 255) {
+        const float sc = e8m0_value(sb);
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          uint32_t o = 0;
+          if (SDT == MOE_F32) {
+            const f32x4 a = __builtin_bit_cast(f32x4, v[(2 * w) % P::PB]), b = __builtin_bit_cast(f32x4, v[(2 * w + 1) % P::PB]);
+            o = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(o, a[0], a[1], sc, 0);
+            o = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(o, a[2], a[3], sc, 1);
+            o = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(o, b[0], b[1], sc, 2);
+            o = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(o, b[2], b[3], sc, 3);
+          } else {
+            const uint32_t p0 = v[w][0], p1 = v[w][1], p2 = v[w][2], p3 = v[w][3];
+            o = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(o, __builtin_bit_cast(bf16x2, p0), sc, 0);
+            o = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(o, __builtin_bit_cast(bf16x2, p1), sc, 1);
+            o = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(o, __builtin_bit_cast(bf16x2, p2), sc, 2);
+            o = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(o, __builtin_bit_cast(bf16x2, p3), sc, 3);
+          }
+          code[w] = o;
+        }
+      }
+      *(u32x4*)(de + at.code + lane * 16) = code;
+      de[at.scale + lane] = (char)sb;
+    }
   }
 }
 
 template <int DDT>
 __global__ __launch_bounds__(256) void entry_dequantize(const char* src, size_t src_stride, int d,
-                                                        int f, char* dst, size_t dst_stride) {
+                                                        int f, char* dst, size_t dst_stride, unsigned ntiles) {
+  using P = Pieces<DDT>;
   typedef float f32x2 __attribute__((ext_vector_type(2)));
-  const unsigned per_mat = (unsigned)((size_t)d * f / 32);
+  __shared__ u32x4 s_p[4][16 * P::PC];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  u32x4* const lp = s_p[wave];
   const char* se = src + blockIdx.y * src_stride;
   char* de = dst + blockIdx.y * dst_stride;
-  for (unsigned g = blockIdx.x * 256 + threadIdx.x; g < 3 * per_mat; g += gridDim.x * 256) {
-    const BlockAt at = block_at(g, per_mat, d, f);
-    const u32x4 c = ldg16(se + at.code);
-    const uint32_t sb = ldg_u8(se + at.scale);
-    const bool nan = sb == 255u;
+  for (unsigned g = blockIdx.x * 4 + wave; g < ntiles; g += gridDim.x * 4) {
+    const TileAt at = tile_at(g, d, f);
+    const int i = lane & 15, q = lane >> 4;
+    const bool has = q < (int)at.blocks;
+    u32x4 code{0u, 0u, 0u, 0u};
+    uint32_t sb = 0;
+    if (has) {
+      code = ldg16_nt(se + at.code + lane * 16);
+      sb = ldg_u8(se + at.scale + lane);
+    }
     const float sc = e8m0_value(sb);
-    char* o = de + at.elem * (DDT == MOE_F32 ? 4 : 2);
+    wave_fence();  // the previous tile's readers are done
+    if (has) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (DDT == MOE_F32) {
-        const f32x2 v0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c[i], sc, 0);
-        const f32x2 v1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c[i], sc, 1);
-        const f32x2 v2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c[i], sc, 2);
-        const f32x2 v3 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c[i], sc, 3);
-        const float q = __uint_as_float(0x7FC00000u);
-        *(f32x4*)(o + 32 * i) = nan ? f32x4{q, q, q, q} : f32x4{v0[0], v0[1], v1[0], v1[1]};
-        *(f32x4*)(o + 32 * i + 16) = nan ? f32x4{q, q, q, q} : f32x4{v2[0], v2[1], v3[0], v3[1]};
-      } else {
-        const u32x4 w{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c[i], sc, 0)),
-                      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c[i], sc, 1)),
-                      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c[i], sc, 2)),
-                      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c[i], sc, 3))};
-        const uint32_t q = 0x7FC07FC0u;
-        *(u32x4*)(o + 16 * i) = nan ? u32x4{q, q, q, q} : w;
+      for (int w = 0; w < 4; ++w) {
+        if (DDT == MOE_F32) {
+          const f32x2 v0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(code[w], sc, 0);
+          const f32x2 v1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(code[w], sc, 1);
+          const f32x2 v2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(code[w], sc, 2);
+          const f32x2 v3 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(code[w], sc, 3);
+          f32x4 a{v0[0], v0[1], v1[0], v1[1]}, b{v2[0], v2[1], v3[0], v3[1]};
+          const float n = __uint_as_float(0x7FC00000u);
+          if (sb == 255u) a = b = f32x4{n, n, n, n};
+          lp[i * P::PC + ((q * P::PB + 2 * w) ^ i)] = __builtin_bit_cast(u32x4, a);
+          lp[i * P::PC + ((q * P::PB + 2 * w + 1) ^ i)] = __builtin_bit_cast(u32x4, b);
+        } else {
+          u32x4 o;
+          o[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(code[w], sc, 0));
+          o[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(code[w], sc, 1));
+          o[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(code[w], sc, 2));
+          o[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(code[w], sc, 3));
+          const uint32_t n = 0x7FC07FC0u;
+          if (sb == 255u) o = u32x4{n, n, n, n};
+          lp[i * P::PC + ((q * P::PB + w) ^ i)] = o;
+        }
+      }
+    }
+    wave_fence();
+    const int sh = (at.blocks == 4 ? 2 : 1) + (DDT == MOE_F32 ? 3 : 2), passes = 16 << sh >> 6;
+    char* o = de + at.elem * P::kElem;
+#pragma unroll
+    for (int r = 0; r < P::PB; ++r) {
+      const int id = r * 64 + lane, row = id >> sh, c = id & ((1 << sh) - 1);
+      if (r < passes) {
+        typedef __attribute__((address_space(1))) u32x4* gout;
+        __builtin_nontemporal_store(lp[row * P::PC + (c ^ row)], (gout)(o + ((size_t)row * at.K * P::kElem + c * 16)));
       }
     }
   }
@@ -119,7 +183,7 @@ __global__ __launch_bounds__(256) void entry_dequantize(const char* src, size_t 
 
 int entry_check(int n, int d, int f, int dt, size_t plain_stride, size_t mx_stride) {
   if (n < 0 || d <= 0 || f <= 0 || d % 64 != 0 || f % 64 != 0) return MOE_EINVAL;
-  if ((size_t)d * f > (size_t)1 << 35) return MOE_EINVAL;  // block numbers are 32-bit
+  if ((size_t)d * f > (size_t)1 << 39) return MOE_EINVAL;  // tile numbers are 32-bit
   if (dt != MOE_F32 && dt != MOE_BF16) return MOE_EUNSUPPORTED;
   if (plain_stride % 16 != 0 || mx_stride % 16 != 0) return MOE_EINVAL;
   if (plain_stride < moe_entry_bytes(d, f, dt) || mx_stride < moe_entry_bytes(d, f, MOE_MXFP4)) return MOE_EINVAL;
@@ -129,8 +193,7 @@ int entry_check(int n, int d, int f, int dt, size_t plain_stride, size_t mx_stri
 // Entries are a grid dimension of their own, at most 65535 of them a launch.
 constexpr int kEntriesPerLaunch = 65535;
 dim3 entry_grid(int n, int d, int f) {
-  const size_t blocks = 3 * ((size_t)d * f / 32);
-  return dim3((unsigned)std::min<size_t>((blocks + 255) / 256, 1 << 15), (unsigned)std::min(n, kEntriesPerLaunch));
+  return dim3((unsigned)std::min<size_t>((entry_tiles(d, f) + 3) / 4, 1 << 14), (unsigned)std::min(n, kEntriesPerLaunch));
 }
 
 }  // namespace
@@ -144,8 +207,8 @@ extern "C" int moe_entry_quantize(const void* src, int src_dtype, size_t src_str
     const dim3 grid = entry_grid(n - i, d, f);
     const char* s = (const char*)src + i * src_stride;
     char* o = (char*)dst + i * dst_stride;
-    if (src_dtype == MOE_F32) hipLaunchKernelGGL(entry_quantize<MOE_F32>, grid, dim3(256), 0, stream, s, src_stride, d, f, o, dst_stride);
-    else hipLaunchKernelGGL(entry_quantize<MOE_BF16>, grid, dim3(256), 0, stream, s, src_stride, d, f, o, dst_stride);
+    if (src_dtype == MOE_F32) hipLaunchKernelGGL(entry_quantize<MOE_F32>, grid, dim3(256), 0, stream, s, src_stride, d, f, o, dst_stride, (unsigned)entry_tiles(d, f));
+    else hipLaunchKernelGGL(entry_quantize<MOE_BF16>, grid, dim3(256), 0, stream, s, src_stride, d, f, o, dst_stride, (unsigned)entry_tiles(d, f));
     MOE_LAUNCH_CHECK();
   }
   return MOE_OK;
@@ -160,8 +223,8 @@ extern "C" int moe_entry_dequantize(const void* src, size_t src_stride, int n, i
     const dim3 grid = entry_grid(n - i, d, f);
     const char* s = (const char*)src + i * src_stride;
     char* o = (char*)dst + i * dst_stride;
-    if (dst_dtype == MOE_F32) hipLaunchKernelGGL(entry_dequantize<MOE_F32>, grid, dim3(256), 0, stream, s, src_stride, d, f, o, dst_stride);
-    else hipLaunchKernelGGL(entry_dequantize<MOE_BF16>, grid, dim3(256), 0, stream, s, src_stride, d, f, o, dst_stride);
+    if (dst_dtype == MOE_F32) hipLaunchKernelGGL(entry_dequantize<MOE_F32>, grid, dim3(256), 0, stream, s, src_stride, d, f, o, dst_stride, (unsigned)entry_tiles(d, f));
+    else hipLaunchKernelGGL(entry_dequantize<MOE_BF16>, grid, dim3(256), 0, stream, s, src_stride, d, f, o, dst_stride, (unsigned)entry_tiles(d, f));
     MOE_LAUNCH_CHECK();
   }
   return MOE_OK;

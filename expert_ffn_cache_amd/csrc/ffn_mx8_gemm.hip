@@ -476,9 +476,9 @@ void m8_tile(FfnArgs p, const uint8_t* ascales, uint32_t last_piece, uint8_t* hs
 
 }  // namespace
 
-// Token rows and h rows are addressed with 32-bit byte offsets.
+// Token rows, h rows and the scales of an entry are addressed with 32-bit byte offsets.
 bool ffn_mx8_gemm_supported(long long T, int k, int d, int f) {
-  return T * d <= (1ll << 32) && T * k * f <= (1ll << 32);
+  return T * d <= (1ll << 32) && T * k * f <= (1ll << 32) && (long long)d * f <= (1ll << 36);
 }
 
 size_t ffn_mx8_plan_bytes(long long A, int E) {
