@@ -32,43 +32,42 @@ constexpr int kM8Ahead = 2;              // weight tiles in flight per wave and 
 constexpr int kM8Codes = 32768;          // LDS bytes of staged codes
 constexpr int kM8Pad = 16;               // bytes between staged rows (bank spread)
 
-// A workgroup's expert and its entry: the a-th active expert in ascending id, found by the first
-// wave from the offsets (256 experts a round trip), or e = -1.
+// A workgroup's expert, its rows and its entry: the a-th active expert in ascending id, found by
+// every wave for itself (the same cached offsets; no barrier), 256 experts a round trip; n = 0 past
+// the last or without an entry.
 struct M8Item {
-  int e;
+  int n0, n;
   const uint8_t* w;
 };
 __device__ __forceinline__ M8Item m8_item(const FfnArgs& p, int a) {
-  __shared__ int s_e;
-  __shared__ const char* s_w;
-  if (threadIdx.x < 64) {
-    const int lane = threadIdx.x;
-    int found = -1, seen = 0;
-    for (int e0 = 0; e0 < p.E && found < 0; e0 += 256) {
-      bool act[4];
+  const int lane = threadIdx.x & 63;
+  int seen = 0;
+  for (int e0 = 0; e0 < p.E; e0 += 256) {
+    int lo[4], hi[4];
+    bool on[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int e = e0 + 64 * j + lane, ec = min(e, p.E - 1);
-        act[j] = active(p, ec) && e < p.E;
-      }
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const unsigned long long m = __ballot(act[j]);
-        const int c = __popcll(m);
-        if (found < 0 && a < seen + c) {
-          const bool mine = act[j] && __popcll(m & lanemask_lt(lane)) == a - seen;
-          found = e0 + 64 * j + __ffsll((long long)__ballot(mine)) - 1;
-        }
-        seen += c;
-      }
+    for (int j = 0; j < 4; ++j) {
+      const int e = min(e0 + 64 * j + lane, p.E - 1);
+      lo[j] = p.offsets[e];
+      hi[j] = p.offsets[e + 1];
+      on[j] = !p.mask || p.mask[e];
     }
-    if (lane == 0) {
-      s_e = found;
-      s_w = found >= 0 ? entry_of(p, found) : nullptr;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int n = hi[j] - lo[j];
+      const bool act = e0 + 64 * j + lane < p.E && n > 0 && n >= p.nmin && n <= p.nmax && on[j];
+      const unsigned long long m = __ballot(act);
+      const int c = __popcll(m);
+      if (a < seen + c) {
+        const bool mine = act && __popcll(m & lanemask_lt(lane)) == a - seen;
+        const int l = __builtin_amdgcn_readfirstlane(__ffsll((long long)__ballot(mine)) - 1);
+        const uint8_t* w = (const uint8_t*)entry_of(p, e0 + 64 * j + l);
+        return M8Item{__builtin_amdgcn_readlane(lo[j], l), w ? __builtin_amdgcn_readlane(n, l) : 0, w};
+      }
+      seen += c;
     }
   }
-  __syncthreads();
-  return M8Item{s_e, (const uint8_t*)s_w};
+  return M8Item{0, 0, nullptr};
 }
 
 __device__ __forceinline__ int m8_rows_class(int n) { return n <= 4 ? 4 : n <= 8 ? 8 : 16; }
@@ -195,8 +194,8 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4))) void m
   const int npair = p.f >> 5, nb = (npair + TR - 1) / TR;
   const int a = blockIdx.x / nb, sb0 = blockIdx.x - a * nb;
   const M8Item it = m8_item(p, a);
-  if (it.e < 0 || !it.w) return;
-  const int n0 = p.offsets[it.e], n = p.offsets[it.e + 1] - n0;
+  const int n0 = it.n0, n = it.n;
+  if (!n) return;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int pr = wave / KS, ks = wave - pr * KS, pair = sb0 * TR + pr;
   const bool work = pair < npair;
@@ -234,8 +233,8 @@ __global__ __launch_bounds__(256) void m8_down(FfnArgs p, const uint8_t* hs) {
   const int npair = p.d >> 5, nb = (npair + TR - 1) / TR;
   const int a = blockIdx.x / nb, sb0 = blockIdx.x - a * nb;
   const M8Item it = m8_item(p, a);
-  if (it.e < 0 || !it.w) return;
-  const int n0 = p.offsets[it.e], n = p.offsets[it.e + 1] - n0;
+  const int n0 = it.n0, n = it.n;
+  if (!n) return;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int pr = wave / KS, ks = wave - pr * KS, pair = sb0 * TR + pr;
   const bool work = pair < npair;
