@@ -42,13 +42,15 @@ constexpr int kMxMaxRows = 16;
 // (T*k / E), MXFP4 experts above kMxGemmMinRowsPerExpert (their streaming path, with the row
 // split above, stays ahead to about 5 rows per expert at Zipf 0.2 and beyond 8 when skewed).
 constexpr long long kGemmMinRowsPerExpert = 2, kMxGemmMinRowsPerExpert = 8;
-// MXFP8 activations: the grouped GEMM above 4 rows per expert on average, weight streaming for
-// every expert up to 32 tokens, split by rows at kMxMaxRows between.  d = 4096, f = 2048, top 6 of
-// 256, Zipf 0.2 / 1, streaming | split | GEMM in us: T = 24 223 / 95 | 232 / 119 | 278 / 82; T = 64
-// 371 / 171 | 381 / 134 | 424 / 133; T = 128 477 / 344 | 525 / 172 | 545 / 149; T = 256 551 / 597 |
-// 598 / 195 | 582 / 192.
-constexpr long long kMx8GemmMinRowsPerExpert = 4;
-constexpr int kMx8MaxT = 32;
+// MXFP8 activations: weight streaming for every expert up to kMx8MaxT tokens, the grouped GEMM
+// above 3 rows per expert on average, between them a split at kMx8MaxRows rows (what one pass of
+// the streaming kernels takes).  d = 4096, f = 2048, top 6 of 256, streaming | split | GEMM in us at
+// Zipf 0.2: T = 32 264 | 272 | 294; T = 64 371 | 381 | 416; T = 128 473 | 488 | 541; T = 170 507 | 524 |
+// 558; at Zipf 1: T = 32 85 | 95 | 85; T = 64 139 | 148 | 133; T = 128 270 | 187 | 149; T = 170 372 | 198
+// | 163.  A split pays the GEMM's launches (about 9 us) where no expert has more rows, and its
+// latency where few do; no split leaves skewed calls at up to twice the time.
+constexpr long long kMx8GemmMinRowsPerExpert = 3;
+constexpr int kMx8MaxT = 32, kMx8MaxRows = 32;
 // Rounds of resident workgroups in the row-split dot-product launches (each loops over items).
 constexpr int kDotSplitRounds = 2;
 
@@ -171,8 +173,8 @@ extern "C" int moe_expert_ffn(const void* x, int act_dtype, const int32_t* perm,
     if (gemm && mx8_gemm_fits) return launch_ffn_mx8_gemm(p, T, y_dtype, stream);
     if (path == MOE_PATH_GEMV || T <= kMx8MaxT || !mx8_gemm_fits) return launch_ffn_mx8(p, T, y_dtype, stream, experts);
     FfnArgs few = p, many = p;
-    few.nmax = kMxMaxRows;
-    many.nmin = kMxMaxRows + 1;
+    few.nmax = kMx8MaxRows;
+    many.nmin = kMx8MaxRows + 1;
     int rc = launch_ffn_mx8(few, T, y_dtype, stream, experts);
     if (rc == MOE_OK) rc = launch_ffn_mx8_gemm(many, T, y_dtype, stream);
     return rc;

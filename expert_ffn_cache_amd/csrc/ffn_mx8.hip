@@ -17,10 +17,12 @@
 // 4, when the strips are too few to fill the chip) share them, tiles ks, ks + KS, ..., their
 // partial sums meeting in LDS.
 //
-// Token rows (at most 16 per pass; experts with more rows make several passes) are staged in
-// LDS over a slice of the contraction that fits 32 KB: 8192 elements for up to 4 rows, 4096 for
-// 8, 2048 for 16; the accumulators carry over from slice to slice.
+// Token rows (at most 16 per pass, 32 in calls of more than 16 tokens, as two token tiles to a weight
+// tile; experts with more rows make several passes) are staged in LDS over a slice of the
+// contraction that fits 32 KB: 8192 elements for up to 4 rows, 4096 for 8, 2048 for 16, 1024 for
+// 32; the accumulators carry over from slice to slice.
 #include <algorithm>
+#include <type_traits>
 
 #include "mx8_dev.h"
 #include "mx_dev.h"
@@ -28,7 +30,10 @@
 namespace moe {
 namespace {
 
-constexpr int kM8Ahead = 2;              // weight tiles in flight per wave and matrix
+// Weight tiles in flight per wave and matrix: two, which leaves four workgroups a CU their
+// registers (64 KB of weights in flight a CU in gate/up); T = 8 101.6 us, with four tiles ahead and two
+// workgroups a CU 105.0.
+constexpr int kM8Ahead = 2;
 constexpr int kM8Codes = 32768;          // LDS bytes of staged codes
 constexpr int kM8Pad = 16;               // bytes between staged rows (bank spread)
 
@@ -70,11 +75,11 @@ __device__ __forceinline__ M8Item m8_item(const FfnArgs& p, int a) {
   return M8Item{0, 0, nullptr};
 }
 
-__device__ __forceinline__ int m8_rows_class(int n) { return n <= 4 ? 4 : n <= 8 ? 8 : 16; }
+__device__ __forceinline__ int m8_rows_class(int n) { return n <= 4 ? 4 : n <= 8 ? 8 : n <= 16 ? 16 : 32; }
 
 // LDS of a workgroup: staged codes with their row padding, then the scales (4 per tile and row).
 struct M8Lds {
-  uint8_t codes[kM8Codes + 16 * kM8Pad];
+  uint8_t codes[kM8Codes + 32 * kM8Pad];
   uint8_t scales[kM8Codes / 32];
 };
 
@@ -99,47 +104,56 @@ __device__ __forceinline__ void m8_stage(M8Lds& lds, const uint8_t* codes, const
   __syncthreads();
 }
 
-template <int NMAT>
-__device__ __forceinline__ void m8_tile_mma(const MxTile<NMAT>& t, const uint8_t* x, uint32_t xs,
-                                            f32x4 (&acc)[NMAT]) {
-  const i32x8 b = fp8_operand(*(const u32x4*)x, *(const u32x4*)(x + 64));
+// acc[r][m] += strip m x token tile r (16 rows each, `next` bytes of codes and of scales further on).
+template <int NMAT, int RT>
+__device__ __forceinline__ void m8_tile_mma(const MxTile<NMAT>& t, const uint8_t* x, int next, const uint8_t* xs,
+                                            int next_s, f32x4 (&acc)[RT][NMAT]) {
 #pragma unroll
-  for (int m = 0; m < NMAT; ++m)
-    acc[m] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fp4_operand(t.c[m]), b, acc[m], 4, 0, 0,
-                                                              (int)t.s[m], 0, (int)xs);
+  for (int r = 0; r < RT; ++r) {
+    const i32x8 b = fp8_operand(*(const u32x4*)(x + r * next), *(const u32x4*)(x + r * next + 64));
+    const int s = xs[r * next_s];
+#pragma unroll
+    for (int m = 0; m < NMAT; ++m)
+      acc[r][m] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fp4_operand(t.c[m]), b, acc[r][m], 4, 0, 0,
+                                                                   (int)t.s[m], 0, s);
+  }
 }
 
 // Partial sums of the KS waves of each strip pair, through the staged rows' LDS: waves ks > 0
 // store, then the first wave adds.
-template <int NMAT, int KS>
-__device__ __forceinline__ void m8_reduce(M8Lds& lds, f32x4 (&acc)[NMAT], int pr, int ks, int lane) {
+template <int RT, int NMAT, int KS>
+__device__ __forceinline__ void m8_reduce(M8Lds& lds, f32x4 (&acc)[RT][NMAT], int pr, int ks, int lane) {
   if (KS == 1) return;
-  f32x4* red = (f32x4*)lds.codes;  // [3][NMAT][64]
+  f32x4* red = (f32x4*)lds.codes;  // [3][RT][NMAT][64]
   __syncthreads();  // the staged rows are read
   if (ks > 0) {
 #pragma unroll
-    for (int m = 0; m < NMAT; ++m) red[((pr * (KS - 1) + ks - 1) * NMAT + m) * 64 + lane] = acc[m];
+    for (int m = 0; m < RT * NMAT; ++m) red[((pr * (KS - 1) + ks - 1) * RT * NMAT + m) * 64 + lane] = acc[m / NMAT][m % NMAT];
   }
   __syncthreads();
   if (ks == 0) {
 #pragma unroll
     for (int j = 1; j < KS; ++j)
 #pragma unroll
-      for (int m = 0; m < NMAT; ++m) acc[m] += red[((pr * (KS - 1) + j - 1) * NMAT + m) * 64 + lane];
+      for (int m = 0; m < RT * NMAT; ++m) acc[m / NMAT][m % NMAT] += red[((pr * (KS - 1) + j - 1) * RT * NMAT + m) * 64 + lane];
   }
 }
 
-// The wave's share of all K for one block of up to 16 rows: acc[m] (+)= strip m x rows.
-template <int NMAT, int KS, typename RowOf>
+// The wave's share of all K for one block of up to 16 RT rows: acc[r][m] = strip m x rows 16 r ...
+template <int NMAT, int KS, int RT, typename RowOf>
 __device__ __forceinline__ void m8_rows(M8Lds& lds, const uint8_t* codes, const uint8_t* scales,
                                         int K, int nt, RowOf src_row, const uint8_t* const (&cb)[NMAT],
                                         const uint8_t* const (&sb)[NMAT], int ks, int lane, bool work,
-                                        f32x4 (&acc)[NMAT]) {
-  const int nk = (K + 127) >> 7, q = lane >> 4, col = min(lane & 15, nt - 1);
+                                        f32x4 (&acc)[RT][NMAT]) {
+  const int nk = (K + 127) >> 7, q = lane >> 4;
+  // rows past the block repeat one (of the last tile): their results are dropped
+  const int row = RT == 1 ? min(lane & 15, nt - 1) : lane & 15, far = RT == 1 ? 0 : min(row + 16, nt - 1) - row;
   const int tps = min(nk, 256 / m8_rows_class(nt));
   const int kshort = (K & 127) ? nk - 1 : -1;
 #pragma unroll
-  for (int m = 0; m < NMAT; ++m) acc[m] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int r = 0; r < RT; ++r)
+#pragma unroll
+    for (int m = 0; m < NMAT; ++m) acc[r][m] = f32x4{0.f, 0.f, 0.f, 0.f};
   for (int t0 = 0; t0 < nk; t0 += tps) {
     const int t1 = min(nk, t0 + tps);
     const int ntw = work && t1 - t0 > ks ? (t1 - t0 - ks + KS - 1) / KS : 0;  // tiles of this wave
@@ -150,14 +164,15 @@ __device__ __forceinline__ void m8_rows(M8Lds& lds, const uint8_t* codes, const 
       if (r < ntw) mx_load_tile<NMAT>(ring[r], cb, sb, kt, lane, kt != kshort || q < 2);
     }
     m8_stage(lds, codes, scales, K, t0, t1, nt, src_row);
-    const uint8_t* xr = lds.codes + col * ((t1 - t0) * 128 + kM8Pad) + 16 * q;
-    const uint8_t* sr = lds.scales + col * (t1 - t0) * 4 + q;
+    const int stride = (t1 - t0) * 128 + kM8Pad, stride_s = (t1 - t0) * 4;
+    const uint8_t* xr = lds.codes + row * stride + 16 * q;
+    const uint8_t* sr = lds.scales + row * stride_s + q;
     for (int i = 0; i < ntw; i += kM8Ahead) {
 #pragma unroll
       for (int r = 0; r < kM8Ahead; ++r) {
         if (i + r < ntw) {
           const int kt = t0 + ks + KS * (i + r);
-          m8_tile_mma<NMAT>(ring[r], xr + (kt - t0) * 128, sr[(kt - t0) * 4], acc);
+          m8_tile_mma<NMAT, RT>(ring[r], xr + (kt - t0) * 128, far * stride, sr + (kt - t0) * 4, far * stride_s, acc);
           const int kn = kt + KS * kM8Ahead;
           if (i + r + kM8Ahead < ntw) mx_load_tile<NMAT>(ring[r], cb, sb, kn, lane, kn != kshort || q < 2);
         }
@@ -187,8 +202,8 @@ __device__ __forceinline__ void m8_store_h(uint8_t* codes, uint8_t* scale, int l
 }
 
 // Gate/up: workgroup = 4/KS pairs of strips (32 units each) of one expert.
-template <int KS>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4))) void m8_gateup(FfnArgs p, const uint8_t* xs, uint8_t* hs) {
+template <int KS, int RT>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(RT == 1 ? 4 : 3))) void m8_gateup(FfnArgs p, const uint8_t* xs, uint8_t* hs) {
   __shared__ __attribute__((aligned(16))) M8Lds lds;
   constexpr int TR = 4 / KS;
   const int npair = p.f >> 5, nb = (npair + TR - 1) / TR;
@@ -206,27 +221,35 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4))) void m
   const uint8_t* const cb[4] = {W + so, W + so + 8 * (size_t)K, W + fd / 2 + so, W + fd / 2 + so + 8 * (size_t)K};
   const uint8_t* const sb[4] = {S + sso, S + sso + K / 2, S + fd / 32 + sso, S + fd / 32 + sso + K / 2};
   const int hss = mxfp8_scale_stride(p.f);
-  for (int m0 = 0; m0 < n; m0 += 16) {
-    const int nt = min(16, n - m0);
-    f32x4 acc[4];
-    m8_rows<4, KS>(lds, (const uint8_t*)p.x, xs, K, nt, [&](int t) { return p.perm[n0 + m0 + t] / p.k; }, cb, sb,
-                   ks, lane, work, acc);
-    m8_reduce<4, KS>(lds, acc, pr, ks, lane);
-    if (ks == 0 && work) {
-      float h[8];
+  for (int m0 = 0; m0 < n; m0 += 16 * RT) {
+    const int nt = min(16 * RT, n - m0);
+    auto block = [&](auto r_tag) {
+      constexpr int NR = decltype(r_tag)::value;
+      f32x4 acc[NR][4];
+      m8_rows<4, KS, NR>(lds, (const uint8_t*)p.x, xs, K, nt, [&](int t) { return p.perm[n0 + m0 + t] / p.k; }, cb, sb,
+                         ks, lane, work, acc);
+      m8_reduce<NR, 4, KS>(lds, acc, pr, ks, lane);
+      if (ks == 0 && work) {
 #pragma unroll
-      for (int s = 0; s < 2; ++s)
+        for (int r = 0; r < NR; ++r) {
+          float h[8];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) h[4 * s + i] = silu(acc[s][i]) * acc[2 + s][i];
-      const int t = lane & 15;
-      const size_t row = (size_t)(n0 + m0 + t);
-      m8_store_h(t < nt ? (uint8_t*)p.h + row * p.f + 32 * pair : nullptr, hs + row * hss + pair, lane, h);
-    }
+          for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) h[4 * s + i] = silu(acc[r][s][i]) * acc[r][2 + s][i];
+          const int t = 16 * r + (lane & 15);
+          const size_t row = (size_t)(n0 + m0 + t);
+          m8_store_h(t < nt ? (uint8_t*)p.h + row * p.f + 32 * pair : nullptr, hs + row * hss + pair, lane, h);
+        }
+      }
+    };
+    if (RT == 2 && nt > 16) block(std::integral_constant<int, RT>{});
+    else block(std::integral_constant<int, 1>{});
   }
 }
 
 // Down: workgroup = 4/KS pairs of strips (32 output channels each) of one expert.
-template <int KS, int YDT>
+template <int KS, int RT, int YDT>
 __global__ __launch_bounds__(256) void m8_down(FfnArgs p, const uint8_t* hs) {
   __shared__ __attribute__((aligned(16))) M8Lds lds;
   constexpr int TR = 4 / KS;
@@ -244,44 +267,72 @@ __global__ __launch_bounds__(256) void m8_down(FfnArgs p, const uint8_t* hs) {
   const uint8_t* S = it.w + 3 * (fd / 2) + 2 * (fd / 32);
   const uint8_t* const cb[2] = {W + so, W + so + 8 * (size_t)K};
   const uint8_t* const sb[2] = {S + sso, S + sso + K / 2};
-  for (int m0 = 0; m0 < n; m0 += 16) {
-    const int nt = min(16, n - m0);
-    f32x4 acc[2];
-    m8_rows<2, KS>(lds, (const uint8_t*)p.h, hs, K, nt, [&](int t) { return n0 + m0 + t; }, cb, sb, ks, lane, work, acc);
-    m8_reduce<2, KS>(lds, acc, pr, ks, lane);
-    const int t = lane & 15, g = lane >> 4;
-    if (ks == 0 && work && t < nt) {
-      const size_t o = (size_t)(n0 + m0 + t) * p.d + 32 * pair + 4 * g;
+  for (int m0 = 0; m0 < n; m0 += 16 * RT) {
+    const int nt = min(16 * RT, n - m0);
+    auto block = [&](auto r_tag) {
+      constexpr int NR = decltype(r_tag)::value;
+      f32x4 acc[NR][2];
+      m8_rows<2, KS, NR>(lds, (const uint8_t*)p.h, hs, K, nt, [&](int t) { return n0 + m0 + t; }, cb, sb, ks, lane, work, acc);
+      m8_reduce<NR, 2, KS>(lds, acc, pr, ks, lane);
+      const int g = lane >> 4;
 #pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        if (YDT == MOE_F32) {
-          *(f32x4*)((float*)p.y + o + 16 * s) = acc[s];
-        } else {
-          *(u32x2*)((uint16_t*)p.y + o + 16 * s) =
-              u32x2{(uint32_t)f32_to_bf16(acc[s][0]) | (uint32_t)f32_to_bf16(acc[s][1]) << 16,
-                    (uint32_t)f32_to_bf16(acc[s][2]) | (uint32_t)f32_to_bf16(acc[s][3]) << 16};
+      for (int r = 0; r < NR; ++r) {
+        const int t = 16 * r + (lane & 15);
+        if (ks != 0 || !work || t >= nt) continue;
+        const size_t o = (size_t)(n0 + m0 + t) * p.d + 32 * pair + 4 * g;
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          const f32x4 v = acc[r][s];
+          if (YDT == MOE_F32) {
+            *(f32x4*)((float*)p.y + o + 16 * s) = v;
+          } else {
+            *(u32x2*)((uint16_t*)p.y + o + 16 * s) = u32x2{(uint32_t)f32_to_bf16(v[0]) | (uint32_t)f32_to_bf16(v[1]) << 16,
+                                                           (uint32_t)f32_to_bf16(v[2]) | (uint32_t)f32_to_bf16(v[3]) << 16};
+          }
         }
       }
-    }
+    };
+    if (RT == 2 && nt > 16) block(std::integral_constant<int, RT>{});
+    else block(std::integral_constant<int, 1>{});
   }
 }
 
-// Waves per strip pair: one unless that leaves fewer than 4 workgroups per CU.
+// Waves per strip pair.  KS waves a pair make KS / 4 workgroups of it, four of which fit a CU: the
+// time is about the rounds of workgroups times a workgroup's share of a strip plus its start-up
+// (about 0.05 of a whole strip), so 1.5 rounds of half strips lose to 3 of quarters, and those to
+// 0.75 of halves (d = 4096, f = 2048, top 6, Zipf 0.2, T = 2, 6, 8, 16, 24: 30.9, 82.2, 94.8, 158, 212 us
+// against 32.6, 85.5, 97.1, 164, 221 for the fewest waves that make four workgroups a CU).
 int m8_ks(int experts, int R) {
-  const long pairs = (long)experts * (R / 32);
-  return pairs / 4 >= 1024 ? 1 : pairs / 2 >= 1024 ? 2 : 4;
+  const long pairs = (long)experts * (R / 32), slots = 4l * num_cus();
+  int best = 1;
+  double least = 1e30;
+  for (int ks = 1; ks <= 4; ks *= 2) {
+    const long wgs = (pairs * ks + 3) / 4;
+    const double t = (double)((wgs + slots - 1) / slots) * (1.0 / ks + 0.05);
+    if (t < least) {
+      least = t;
+      best = ks;
+    }
+  }
+  return best;
 }
 
 template <int KS>
-void launch_gu(const FfnArgs& p, const uint8_t* xs, uint8_t* hs, int experts, hipStream_t stream) {
-  const int nb = (p.f / 32 * KS + 3) / 4;
-  hipLaunchKernelGGL(m8_gateup<KS>, dim3(experts * nb), dim3(256), 0, stream, p, xs, hs);
+void launch_gu(const FfnArgs& p, const uint8_t* xs, uint8_t* hs, int experts, bool wide, hipStream_t stream) {
+  const dim3 grid(experts * ((p.f / 32 * KS + 3) / 4));
+  if (wide) hipLaunchKernelGGL((m8_gateup<KS, 2>), grid, dim3(256), 0, stream, p, xs, hs);
+  else hipLaunchKernelGGL((m8_gateup<KS, 1>), grid, dim3(256), 0, stream, p, xs, hs);
+}
+template <int KS, int RT>
+void launch_dn_rt(const FfnArgs& p, const uint8_t* hs, int y_dtype, int experts, hipStream_t stream) {
+  const dim3 grid(experts * ((p.d / 32 * KS + 3) / 4));
+  if (y_dtype == MOE_F32) hipLaunchKernelGGL((m8_down<KS, RT, MOE_F32>), grid, dim3(256), 0, stream, p, hs);
+  else hipLaunchKernelGGL((m8_down<KS, RT, MOE_BF16>), grid, dim3(256), 0, stream, p, hs);
 }
 template <int KS>
-void launch_dn(const FfnArgs& p, const uint8_t* hs, int y_dtype, int experts, hipStream_t stream) {
-  const dim3 grid(experts * ((p.d / 32 * KS + 3) / 4));
-  if (y_dtype == MOE_F32) hipLaunchKernelGGL((m8_down<KS, MOE_F32>), grid, dim3(256), 0, stream, p, hs);
-  else hipLaunchKernelGGL((m8_down<KS, MOE_BF16>), grid, dim3(256), 0, stream, p, hs);
+void launch_dn(const FfnArgs& p, const uint8_t* hs, int y_dtype, int experts, bool wide, hipStream_t stream) {
+  if (wide) launch_dn_rt<KS, 2>(p, hs, y_dtype, experts, stream);
+  else launch_dn_rt<KS, 1>(p, hs, y_dtype, experts, stream);
 }
 
 }  // namespace
@@ -290,16 +341,17 @@ int launch_ffn_mx8(const FfnArgs& p, int T, int y_dtype, hipStream_t stream, int
   if (experts <= 0) return MOE_OK;
   const uint8_t* xs = (const uint8_t*)p.x + (size_t)T * p.d;
   uint8_t* hs = (uint8_t*)p.h + (size_t)T * p.k * p.f;
+  const bool wide = T > 16;  // an expert has at most T rows
   switch (m8_ks(experts, p.f)) {
-    case 1: launch_gu<1>(p, xs, hs, experts, stream); break;
-    case 2: launch_gu<2>(p, xs, hs, experts, stream); break;
-    default: launch_gu<4>(p, xs, hs, experts, stream); break;
+    case 1: launch_gu<1>(p, xs, hs, experts, wide, stream); break;
+    case 2: launch_gu<2>(p, xs, hs, experts, wide, stream); break;
+    default: launch_gu<4>(p, xs, hs, experts, wide, stream); break;
   }
   MOE_LAUNCH_CHECK();
   switch (m8_ks(experts, p.d)) {
-    case 1: launch_dn<1>(p, hs, y_dtype, experts, stream); break;
-    case 2: launch_dn<2>(p, hs, y_dtype, experts, stream); break;
-    default: launch_dn<4>(p, hs, y_dtype, experts, stream); break;
+    case 1: launch_dn<1>(p, hs, y_dtype, experts, wide, stream); break;
+    case 2: launch_dn<2>(p, hs, y_dtype, experts, wide, stream); break;
+    default: launch_dn<4>(p, hs, y_dtype, experts, wide, stream); break;
   }
   MOE_LAUNCH_CHECK();
   return MOE_OK;
