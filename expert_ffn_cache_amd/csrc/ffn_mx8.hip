@@ -31,7 +31,7 @@ namespace moe {
 namespace {
 
 // Weight tiles in flight per wave and matrix: two, which leaves four workgroups a CU their
-// registers (64 KB of weights in flight a CU in gate/up); T = 8 101.6 us, with four tiles ahead and two
+// registers (128 KB of weights in flight a CU in gate/up); T = 8 101.6 us, with four tiles ahead and two
 // workgroups a CU 105.0.
 constexpr int kM8Ahead = 2;
 constexpr int kM8Codes = 32768;          // LDS bytes of staged codes

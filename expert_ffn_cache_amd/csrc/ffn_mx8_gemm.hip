@@ -16,9 +16,9 @@
 // selects.  Token rows lie at 128 bytes with their 16-byte pieces permuted by (row / 2) mod 8
 // (16 lanes that read one piece of 16 rows then touch all banks once).
 //
-// Work list: persistent workgroups over (expert, weight tile, token tile), derived from the
-// offsets on the device; consecutive items, which share weights or token rows, go to one XCD.
-// Token tiles go four at a time to a weight tile, so its codes come from L2 for three of them.
+// Work list: a small kernel lists the experts' token tiles from the offsets and cuts the list into a
+// share for each XCD; persistent workgroups draw (token tile, weight tile) items from their XCD's
+// queue, so items that run together share token rows or weights in its L2.
 #include <algorithm>
 #include <type_traits>
 
@@ -91,7 +91,7 @@ __host__ __device__ constexpr int plan_counter(int mode, int xcd) { return 16 * 
 // what an item costs beside them.
 __device__ __forceinline__ int plan_cost(int rows) { return (rows + 31) / 32 + 2; }
 
-__global__ __launch_bounds__(kMaxE) void m8_plan(FfnArgs p, int* plan) {
+__global__ __launch_bounds__(kMaxE) void m8_plan(FfnArgs p, int* plan, int drawn) {
   __shared__ int s_first[kMaxE + 1];
   __shared__ long long s_before[kMaxE];
   __shared__ int s_cnt[kMaxE / 64];
@@ -115,7 +115,7 @@ __global__ __launch_bounds__(kMaxE) void m8_plan(FfnArgs p, int* plan) {
     s_cnt[wave] = x;
     s_cost[wave] = y;
   }
-  if (e < 16) plan[16 * e] = 0;
+  if (e < 16) plan[16 * e] = drawn;  // every workgroup begins with the item of its place in its XCD
   __syncthreads();
   int first = x - tiles, all = 0;
   long long before = y - cost, total = 0;
@@ -168,8 +168,9 @@ void m8_tile(FfnArgs p, const uint8_t* ascales, uint32_t last_piece, uint8_t* hs
   const uint8_t* acodes = (const uint8_t*)(MODE == 0 ? p.x : p.h);
 
   // Items of this XCD's share first, then of the others', so no workgroup stops early; a share's
-  // queue runs over its token tiles, four of them to a weight tile.  The next item is drawn while
-  // the current one is computed.
+  // queue runs over its token tiles and, for each, over the weight tiles (2 to 16 token tiles to a
+  // weight tile, for its codes to come from L2, are 0 to 5% slower at T = 8192: workgroups drift).
+  // The next item is drawn while the current one is computed.
   const int* const share = plan + kPlanShares;
   const PlanTile* const tiles = (const PlanTile*)(plan + kPlanTiles);
   auto share_items = [&](int q) { return (share[q + 1] - share[q]) * n_ntiles; };
@@ -201,21 +202,15 @@ void m8_tile(FfnArgs p, const uint8_t* ascales, uint32_t last_piece, uint8_t* hs
     }
   };
   // drawn ahead: held by lane 0 of wave 0
-  int next_q = blockIdx.x & 7, next_j = 0;
-  if (wave == 0) {
-    const int n = share_items(next_q);
-    if (lane == 0) next_j = n > 0 ? draw(next_q) : 0;
-    settle(next_q, __shfl(next_j, 0));
-  }
+  int next_q = 0, next_j = 0;
+  if (wave == 0) settle(blockIdx.x & 7, blockIdx.x >> 3);
   __syncthreads();
 
   for (;;) {
     const int q = s_item[0], j = s_item[1];
     if (q < 0) return;
-    const int m_0 = share[q], m_n = share[q + 1] - m_0;
-    const int grp = j / (4 * n_ntiles), gsz = min(4, m_n - grp * 4), in = j - grp * 4 * n_ntiles;
-    const int nt = in / gsz;
-    const PlanTile tile = tiles[m_0 + grp * 4 + (in - nt * gsz)];
+    const int m = j / n_ntiles, nt = j - m * n_ntiles;
+    const PlanTile tile = tiles[share[q] + m];
     const int n0 = tile.n0, rows = tile.rows;
     const uint8_t* W = (const uint8_t*)entry_of(p, tile.e);
     __syncthreads();  // the item is read, and the previous one's readers of the LDS are done
@@ -494,7 +489,7 @@ int launch_ffn_mx8_gemm(const FfnArgs& p, int T, int y_dtype, hipStream_t stream
   const dim3 grid((num_cus() * 2 + 7) / 8 * 8), blk(256);
   const int ntd = (p.d + 255) / 256;
   const uint32_t last_x = (uint32_t)((size_t)T * p.d - 16), last_h = (uint32_t)(A * p.f - 16);
-  hipLaunchKernelGGL(m8_plan, dim3(1), dim3(kMaxE), 0, stream, p, plan);
+  hipLaunchKernelGGL(m8_plan, dim3(1), dim3(kMaxE), 0, stream, p, plan, (int)grid.x / 8);
   MOE_LAUNCH_CHECK();
   hipLaunchKernelGGL((m8_tile<0, MOE_BF16>), grid, blk, 0, stream, p, xs, last_x, hs, (p.f + 127) / 128, plan);
   MOE_LAUNCH_CHECK();

@@ -342,7 +342,11 @@ PATHS = [moe.MOE_PATH_AUTO, moe.MOE_PATH_GEMV, moe.MOE_PATH_GEMM]
     (13, 37, 4, 1088, 320, 0.5),   # short last tiles on both sides
     (64, 16, 4, 320, 448, 1.0),
     (200, 5, 3, 256, 576, 1.0),    # over 100 rows for an expert
-    (700, 3, 1, 128, 128, 0.2)])   # several 256-row tiles
+    (700, 3, 1, 128, 128, 0.2),    # several 128-row tiles
+    (2, 4, 2, 8320, 64, 0.2),      # token rows staged over two slices of K, gate/up and down
+    (2, 4, 2, 64, 8320, 0.2),
+    (9, 4, 2, 4224, 64, 0.2),
+    (40, 4, 2, 1088, 64, 0.2)])
 def test_ffn_mxfp8(T, E, k, d, f, alpha, path, ydt):
     w = _mx_workload(T, E, k, d, f, alpha)
     x, x8, perm, offsets, ids = _case(w)
@@ -351,6 +355,48 @@ def test_ffn_mxfp8(T, E, k, d, f, alpha, path, ydt):
     assert st == 0
     ref, tol = mx8.expert_ffn(x, perm, k, offsets, _mx_weights(w, range(E)))
     _check_ffn(y, ydt, ref, tol)
+
+
+@pytest.mark.parametrize("T,d,f", [(64, 128, 2048), (64, 2048, 128), (16, 128, 2048), (16, 2048, 128),
+                                   (3, 128, 2048)])
+def test_ffn_mxfp8_waves_per_strip(T, d, f):
+    """256 experts: enough strips for one and two waves to a strip pair, at up to 16 rows a pass and
+    up to 32 (fewer experts take four)."""
+    w = _mx_workload(T, 256, 6, d, f, 0.2)
+    x, x8, perm, offsets, ids = _case(w)
+    arena = device_arena_all_experts(w)
+    y, st = _ffn(w, x8, dev(perm), dev(offsets), arena, w.entry_bytes, moe.MOE_F32, moe.MOE_PATH_GEMV)
+    assert st == 0
+    used = sorted(set(ids.ravel().tolist()))[::5]
+    rows = np.zeros(T * w.k, dtype=bool)
+    for e in used:
+        rows[offsets[e]:offsets[e + 1]] = True
+    ref, tol = mx8.expert_ffn(x, perm, w.k, offsets, _mx_weights(w, used))
+    _check_ffn(y, moe.MOE_F32, ref, tol, rows)
+
+
+@pytest.mark.parametrize("T", [1, 20, 100, 600])
+def test_ffn_mxfp8_at_maximum_experts_and_k(T):
+    w = _mx_workload(T, 1024, 16, 128, 64)
+    x, x8, perm, offsets, ids = _case(w)
+    arena = device_arena_all_experts(w)
+    ref, tol = mx8.expert_ffn(x, perm, w.k, offsets, _mx_weights(w, sorted(set(ids.ravel().tolist()))))
+    for path in PATHS:
+        y, st = _ffn(w, x8, dev(perm), dev(offsets), arena, w.entry_bytes, moe.MOE_F32, path)
+        assert st == 0
+        _check_ffn(y, moe.MOE_F32, ref, tol)
+
+
+@pytest.mark.parametrize("path", PATHS)
+@pytest.mark.parametrize("T", [5, 50, 300])
+def test_ffn_mxfp8_without_any_expert(T, path):
+    """Every expert masked: nothing is written."""
+    w = _mx_workload(T, 8, 2, 128, 64)
+    x, x8, perm, offsets, ids = _case(w)
+    arena = device_arena_all_experts(w)
+    mask = torch.zeros(w.E, dtype=torch.uint8, device="cuda")
+    y, st = _ffn(w, x8, dev(perm), dev(offsets), arena, w.entry_bytes, moe.MOE_F32, path, mask)
+    assert st == 0 and bool(torch.isnan(y).all())
 
 
 def _ids_with(counts, T, k):

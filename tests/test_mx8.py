@@ -148,6 +148,10 @@ def test_expert_ffn_with_mxfp8_activations_refuses():
     assert rc(_11=eb - 16) == EINVAL and rc(_7=4000) == EINVAL and rc(_0=None) == EINVAL
     assert rc(_0=A + 8) == EINVAL and rc(_20=3) == EINVAL
     assert rc(_4=0) == 0
+    # the grouped GEMM keeps byte offsets of token rows in 32 bits: an explicit request past that is
+    # refused, AUTO takes the streaming kernels (accepted up to the null buffers)
+    assert rc(_4=1 << 21, _5=1, _20=moe.MOE_PATH_GEMM, _0=None) == EUNSUP
+    assert rc(_4=1 << 21, _5=1, _20=moe.MOE_PATH_AUTO, _0=None) == EINVAL
     # the no-allocation form: T*k*(f + scales) beyond its array
     T = moe.moe_expert_ffn_noalloc_max_bytes() // (2048 + 64) + 1
     na = [A, X8, A, A, T, 1, 256, 4096, 2048, None, A, eb, X4, None, None, 0, A, F32, 0, None, None]
