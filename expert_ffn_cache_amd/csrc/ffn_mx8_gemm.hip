@@ -268,11 +268,11 @@ void m8_tile(FfnArgs p, const uint8_t* ascales, uint32_t last_piece, uint8_t* hs
 #pragma unroll
       for (int t = 0; t < 4; ++t)
         if (hh == t / 2)
-        g_load16(acodes, min(oa[t] + (uint32_t)kt * 128, last_piece), st + kGTokAt + (4 * wave + t) * 1024);
+          g_load16(acodes, min(oa[t] + (uint32_t)kt * 128, last_piece), st + kGTokAt + (4 * wave + t) * 1024);
 #pragma unroll
       for (int s = 0; s < 4; ++s)
         if (hh == s / 2)
-        g_load16(c0 + (s & 1) * strip + (s >> 1) * second, oc, st + kGCodeAt + (wave * 4 + s) * 1024);
+          g_load16(c0 + (s & 1) * strip + (s >> 1) * second, oc, st + kGCodeAt + (wave * 4 + s) * 1024);
     };
     using H0 = std::integral_constant<int, 0>;
     using H1 = std::integral_constant<int, 1>;
@@ -484,7 +484,7 @@ int launch_ffn_mx8_gemm(const FfnArgs& p, int T, int y_dtype, hipStream_t stream
   const uint8_t* xs = (const uint8_t*)p.x + (size_t)T * p.d;
   const size_t A = (size_t)T * p.k;
   uint8_t* hs = (uint8_t*)p.h + A * p.f;
-  int* plan = (int*)(hs + (A * mxfp8_scale_stride(p.f) + 255) / 256 * 256);
+  int* plan = (int*)((uint8_t*)p.h + (A * (p.f + mxfp8_scale_stride(p.f)) + 255) / 256 * 256);
   // two workgroups a CU: the hand-off of a stage in one is covered by the other's products
   const dim3 grid((num_cus() * 2 + 7) / 8 * 8), blk(256);
   const int ntd = (p.d + 255) / 256;

@@ -425,6 +425,20 @@ def test_ffn_mxfp8_row_counts(counts, T, k, path):
     _check_ffn(y, moe.MOE_F32, ref, tol)
 
 
+@pytest.mark.parametrize("path", PATHS)
+@pytest.mark.parametrize("T,k", [(15, 1), (31, 1), (11, 3)])
+def test_ffn_mxfp8_work_list_of_single_rows_ends_with_its_workspace(T, k, path):
+    """Every row an expert of its own (the longest work list for its rows), sizes at which the
+    intermediate ends on an odd multiple of 64 bytes."""
+    w = _mx_workload(T, 40, k, 128, 64)
+    x, x8, perm, offsets, ids = _case(w, np.arange(T * k, dtype=np.int32).reshape(T, k))
+    arena = device_arena_all_experts(w)
+    y, st = _ffn(w, x8, dev(perm), dev(offsets), arena, w.entry_bytes, moe.MOE_F32, path)
+    assert st == 0
+    ref, tol = mx8.expert_ffn(x, perm, k, offsets, _mx_weights(w, range(w.E)))
+    _check_ffn(y, moe.MOE_F32, ref, tol)
+
+
 @pytest.mark.parametrize("T,d,f,alpha", [(1, 4096, 2048, 0.2), (8, 4096, 2048, 0.2), (24, 4096, 2048, 1.0)])
 def test_ffn_mxfp8_decode_layer(T, d, f, alpha):
     """The decode layer's own sizes: the rows of six experts against the definition."""
