@@ -183,7 +183,8 @@ __global__ __launch_bounds__(256) void entry_dequantize(const char* src, size_t 
 
 int entry_check(int n, int d, int f, int dt, size_t plain_stride, size_t mx_stride) {
   if (n < 0 || d <= 0 || f <= 0 || d % 64 != 0 || f % 64 != 0) return MOE_EINVAL;
-  if ((size_t)d * f > (size_t)1 << 39) return MOE_EINVAL;  // tile numbers are 32-bit
+  // tile numbers are 32-bit, element numbers of a row ints
+  if ((size_t)d * f > (size_t)1 << 39 || std::max(d, f) > 0x7FFFFFFF - 127) return MOE_EINVAL;
   if (dt != MOE_F32 && dt != MOE_BF16) return MOE_EUNSUPPORTED;
   if (plain_stride % 16 != 0 || mx_stride % 16 != 0) return MOE_EINVAL;
   if (plain_stride < moe_entry_bytes(d, f, dt) || mx_stride < moe_entry_bytes(d, f, MOE_MXFP4)) return MOE_EINVAL;

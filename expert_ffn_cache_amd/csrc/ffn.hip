@@ -51,6 +51,7 @@ constexpr long long kGemmMinRowsPerExpert = 2, kMxGemmMinRowsPerExpert = 8;
 // latency where few do; no split leaves skewed calls at up to twice the time.
 constexpr long long kMx8GemmMinRowsPerExpert = 3;
 constexpr int kMx8MaxT = 32, kMx8MaxRows = 32;
+constexpr int kMx8MaxDim = 0x7FFFFFFF - 127;  // element numbers to the end of a row's last tile are ints
 // Rounds of resident workgroups in the row-split dot-product launches (each loops over items).
 constexpr int kDotSplitRounds = 2;
 
@@ -148,6 +149,7 @@ extern "C" int moe_expert_ffn(const void* x, int act_dtype, const int32_t* perm,
   }
   const bool bf16_gemm_fits = ffn_gemm_supported(T, k, d, f);
   if (w_dtype == MOE_BF16 && path == MOE_PATH_GEMM && !bf16_gemm_fits) return MOE_EUNSUPPORTED;
+  if (act_dtype == MOE_MXFP8 && std::max(d, f) > kMx8MaxDim) return MOE_EUNSUPPORTED;
   const bool mx8_gemm_fits = ffn_mx8_gemm_supported(T, k, d, f);
   if (act_dtype == MOE_MXFP8 && path == MOE_PATH_GEMM && !mx8_gemm_fits) return MOE_EUNSUPPORTED;
   const size_t need = mx ? moe_entry_bytes(d, f, w_dtype) : 3 * (size_t)d * f * (f32 ? 4 : 2);

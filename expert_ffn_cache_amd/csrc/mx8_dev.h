@@ -16,7 +16,7 @@ namespace moe {
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef short i16x2 __attribute__((ext_vector_type(2)));
 
-__host__ __device__ constexpr int mxfp8_scale_stride(int d) { return (d + 127) / 128 * 4; }
+__host__ __device__ constexpr int mxfp8_scale_stride(int d) { return (int)(((unsigned)d + 127) / 128 * 4); }
 
 __device__ __forceinline__ float e8m0_value(uint32_t s) {
   return s ? __uint_as_float(s << 23) : __uint_as_float(0x00400000u);  // 2^(s - 127)

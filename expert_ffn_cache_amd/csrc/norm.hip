@@ -15,6 +15,7 @@
 // 63.4 us, 5.1 TB/s).  Longer rows take four chunks a thread, and past 32768 elements a loop that
 // reads s back in a second pass.
 #include <algorithm>
+#include <limits>
 
 #include "mx8_dev.h"
 #include "wave.h"
@@ -208,14 +209,14 @@ template <int DM>
 __global__ __launch_bounds__(1024) void rmsnorm_long(NormArgs p) {
   const int t = p.t0 + (int)blockIdx.x;
   float ss = 0.f;
-  for (int c = threadIdx.x * 8; c < p.d; c += 1024 * 8) {
+  for (unsigned c = threadIdx.x * 8; c < (unsigned)p.d; c += 1024 * 8) {
     const F8 s = load_sum<DM>(p, t, c);
     if (p.x_out) store8(p.x_out, (size_t)t * p.d + c, p.x_dt, s);
 #pragma unroll
     for (int q = 0; q < 8; ++q) ss = fmaf(s.v[q], s.v[q], ss);
   }
   const float rstd = row_rstd(row_sum<1024>(ss), p.d, p.eps);
-  for (int c = threadIdx.x * 8; c < p.d; c += 1024 * 8) {
+  for (unsigned c = threadIdx.x * 8; c < (unsigned)p.d; c += 1024 * 8) {
     const F8 s = p.x_out ? load8(p.x_out, (size_t)t * p.d + c, p.x_dt) : load_sum<DM>(p, t, c);
     norm_out(p, t, c, s, rstd);
   }
@@ -249,7 +250,7 @@ bool real_type(int dt) { return dt == MOE_F32 || dt == MOE_BF16; }
 // Checks shared by both norms: sizes and types, then (T > 0) pointers.
 int norm_check(const NormArgs& p) {
   if (p.T < 0 || p.d <= 0 || p.d % 64 != 0) return MOE_EINVAL;
-  if (!(p.eps >= 0.f) || p.eps > 3e38f) return MOE_EINVAL;
+  if (!(p.eps >= 0.f && p.eps <= std::numeric_limits<float>::max())) return MOE_EINVAL;
   if (!real_type(p.x_dt) || !real_type(p.gamma_dt) || (p.y && !real_type(p.y_dt))) return MOE_EUNSUPPORTED;
   return MOE_OK;
 }

@@ -162,8 +162,8 @@ size_t moe_entry_bytes(int d, int f, int w_dtype);
  * holds an infinity or a NaN gets the scale byte 255, which stands for NaN in every element.
  * moe_entry_dequantize: the values (E2M1 value x scale, exact in both types but for bf16 /
  * fp32 underflow below 2^-133 / 2^-149, which no scale reaches), scale byte 255 as NaN.
- * Device memory, 16-byte aligned, as are the strides; strides at least the entry's bytes; src
- * and dst must not overlap.  Bytes between entries are left as they are. */
+ * Device memory, 16-byte aligned, as are the strides; strides at least the entry's bytes, d*f
+ * at most 2^39; src and dst must not overlap.  Bytes between entries are left as they are. */
 int moe_entry_quantize(const void* src, int src_dtype, size_t src_stride, int n, int d, int f,
                        void* dst, size_t dst_stride, hipStream_t stream);
 int moe_entry_dequantize(const void* src, size_t src_stride, int n, int d, int f, void* dst,
@@ -181,7 +181,8 @@ size_t moe_mxfp8_bytes(int T, int d);
  * floor(log2 max|V|) - 8 + 127, at least 0 (also for an all-zero block); each element
  * V/2^(s-127) to the nearest E4M3 value, ties to even, magnitudes beyond 448 saturating to
  * 448; a block that holds an infinity or a NaN gets scale 255 and codes 0x7F and stands for
- * NaN in every element.  Back: code value x scale (rounded only where bf16 underflows). */
+ * NaN in every element.  Back: code value x scale (rounded only where bf16 underflows).  x and x8
+ * are 16-byte aligned and must not overlap. */
 int moe_mxfp8_quantize(const void* x, int x_dtype, int T, int d, void* x8, hipStream_t stream);
 int moe_mxfp8_dequantize(const void* x8, int T, int d, void* x, int x_dtype, hipStream_t stream);
 
@@ -227,7 +228,9 @@ size_t moe_expert_ffn_workspace_bytes(int T, int k, int f, int act_dtype);
  *  weights the activations may also be MOE_MXFP8: x is then an MXFP8 buffer of T rows (see
  *  moe_mxfp8_bytes), y fp32 or bf16; the products take the codes and scales of both sides as
  *  they are (block-scaled matrix instructions, fp32 accumulation), and h is rounded to MXFP8
- *  (as by moe_mxfp8_quantize) before the down projection.  MXFP4 with MOE_BF16 runs
+ *  (as by moe_mxfp8_quantize) before the down projection; d and f below 2^31 - 127, the GEMM
+ *  path's T*d and T*k*f each <= 2^32 and d*f <= 2^36 (MOE_EUNSUPPORTED past that; auto stays
+ *  on the weight-streaming path).  MXFP4 with MOE_BF16 runs
  *  on both paths (the weight-streaming one for d, f <= 8128).  With MOE_BF16
  *  weights the GEMM path needs T*d, T*k*f and 3*d*f each <= 2^32 (it keeps
  *  element offsets in 32 bits): MOE_PATH_GEMM past that returns

@@ -109,6 +109,21 @@ def test_rmsnorm_refuses(change, want):
     assert L.moe_combine_rmsnorm(a["delta"], a["ddt"], A, A, 2, *tail) == want
 
 
+def test_rmsnorm_takes_every_finite_eps():
+    largest = float(np.finfo(np.float32).max)
+    assert moe.lib().moe_rmsnorm(A, BF16, None, BF16, A, BF16, largest, 0, 128, None, A, BF16, None, None) == 0
+
+
+@pytest.mark.parametrize("d,f", [((1 << 31) - 64, 64), (64, (1 << 31) - 64)])
+def test_rows_whose_last_tile_passes_31_bits_are_refused(d, f):
+    L = moe.lib()
+    for path in range(3):
+        assert L.moe_expert_ffn(A, X8, A, A, 1, 1, 1, d, f, None, A, 1 << 50, X4, None, None, 0, A, 1 << 50, A, F32,
+                                path, A, None) == EUNSUP
+    assert L.moe_entry_quantize(A, BF16, 1 << 50, 1, d, f, A, 1 << 50, None) == EINVAL
+    assert L.moe_entry_dequantize(A, 1 << 50, 1, d, f, A, BF16, 1 << 50, None) == EINVAL
+
+
 def test_combine_rmsnorm_refuses_its_own():
     tail = (A, BF16, A, BF16, 1e-6, 4, 128, A, A, BF16, A, None)
     L = moe.lib()
