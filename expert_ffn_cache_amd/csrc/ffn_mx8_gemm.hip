@@ -31,14 +31,21 @@ constexpr int kGCodes = 16 * 1024;       // codes of a stage: strip s at s * 102
 constexpr int kGScales = 16 * 64;        // weight scales of a stage: strip s at s * 64
 
 constexpr int kGM = 128;                 // token rows of a tile
-// A stage: weight scales, token rows (row r at r * 128), codes.
-constexpr int kGTokAt = kGScales;
-constexpr int kGCodeAt = kGTokAt + kGM * 128;
-constexpr int kGStage = kGCodeAt + kGCodes;
+// A stage: weight scales, codes, token rows (row r at r * 128).
+constexpr int kGCodeAt = kGScales;
+constexpr int kGTokAt = kGCodeAt + kGCodes;
+// The ring of a tile of AM blocks of 32 rows: three stages up to 64 rows, where a step's products are
+// shorter than a load takes, two above, where the LDS (two workgroups a CU) holds no more.  d = 4096,
+// f = 2048, top 6 of 256, Zipf 1, T = 64 and 512: 112 and 226 us, with two stages 131 and 256.
+constexpr int kGFew = 2;
+constexpr int g_stages(int am) { return am <= kGFew ? 3 : 2; }
+constexpr int g_stage(int am) { return kGTokAt + (am <= kGFew ? kGFew : kGM / 32) * 32 * 128; }
+constexpr int g_rows(int am) { return (am <= kGFew ? kGFew : kGM / 32) * 32; }
 // Token scales come in chunks of 8 steps, two of them in LDS: row r's word of step n of a chunk at
 // word r * 8 + (n ^ (r / 8) mod 8).  One load brings 8 rows x 32 bytes; a word per row and step
 // instead would fetch a whole cache line for it (that alone cost half of the time).
-constexpr int kGTsWords = kGM * 8;
+constexpr int g_lds_bytes(int am) { return g_stages(am) * g_stage(am) + 2 * 32 * g_rows(am); }
+constexpr int kGLds = g_lds_bytes(1) > g_lds_bytes(4) ? g_lds_bytes(1) : g_lds_bytes(4);
 
 __device__ __forceinline__ uint32_t g_lds_addr(const void* p) {
   return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)p;
@@ -153,9 +160,8 @@ __global__ __launch_bounds__(kMaxE) void m8_plan(FfnArgs p, int* plan, int drawn
 template <int MODE, int YDT>  // MODE 0: gate/up (h out), 1: down (y out)
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2)))
 void m8_tile(FfnArgs p, const uint8_t* ascales, uint32_t last_piece, uint8_t* hscales, int n_ntiles, int* plan) {
-  __shared__ __attribute__((aligned(1024))) uint8_t sm[2][kGStage];
+  __shared__ __attribute__((aligned(1024))) uint8_t sm[kGLds];
   __shared__ int s_item[2];  // an XCD's share and the item in its queue, -1: none left
-  __shared__ __attribute__((aligned(256))) uint32_t s_ts[2][kGTsWords];
   __shared__ uint32_t s_row[kGM];  // where the tile's token rows' scales start
 
   const int tid = threadIdx.x, lane = tid & 63;
@@ -164,7 +170,7 @@ void m8_tile(FfnArgs p, const uint8_t* ascales, uint32_t last_piece, uint8_t* hs
   const int nk = (K + 127) >> 7, ss = mxfp8_scale_stride(K);
   const bool half = (K & 127) != 0;  // the last step holds 64 elements
   const size_t fd = (size_t)p.f * p.d;
-  const uint32_t lds_sm = g_lds_addr(sm), lds_ts = g_lds_addr(s_ts);
+  const uint32_t lds_sm = g_lds_addr(sm);
   const uint8_t* acodes = (const uint8_t*)(MODE == 0 ? p.x : p.h);
 
   // Items of this XCD's share first, then of the others', so no workgroup stops early; a share's
@@ -224,18 +230,7 @@ void m8_tile(FfnArgs p, const uint8_t* ascales, uint32_t last_piece, uint8_t* hs
     int ln = lane;
     asm volatile("" : "+v"(ln));  // keeps what follows from the lane out of the loops' live registers
 
-    // A wave loads 32 token rows (four loads of 8 rows, a lane's 16-byte piece permuted), the codes
-    // and the scales of its own four strips, and a load of the next token scale chunk: no branch,
-    // the same ten loads in each wave.  In a last step of 64 elements the second half of a code tile
-    // and of its scales does not exist (the first is read twice); the pieces of token rows past
-    // their end are other rows' or, at the buffer's last row, its last bytes.  None of that is used.
     auto row_at = [&](int r) { return (uint32_t)(MODE == 0 ? p.perm[n0 + r] / p.k : n0 + r); };
-    uint32_t oa[4];
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      const int r = (4 * wave + t) * 8 + (ln >> 3);
-      oa[t] = row_at(min(r, rows - 1)) * (uint32_t)K + ((ln & 7) ^ ((r >> 1) & 7)) * 16;
-    }
     // the wave's strips: 32 units of gate and of up, or 64 output channels (past the matrix:
     // the first ones, their results dropped)
     int r0 = MODE == 0 ? nt * 128 + wave * 32 : nt * 256 + wave * 64;
@@ -245,48 +240,7 @@ void m8_tile(FfnArgs p, const uint8_t* ascales, uint32_t last_piece, uint8_t* hs
     const uint8_t* const wscales = W + 3 * (fd / 2) + (MODE == 0 ? 0 : 2 * (fd / 32)) + (size_t)r0 * (K / 32);
     const size_t strip = (size_t)K * 8, second = MODE == 0 ? fd / 2 : 2 * strip;
     const uint32_t ows = ((ln >> 4) & 1) * (K / 2) + (ln >> 5) * (uint32_t)(MODE == 0 ? fd / 32 : K) + (ln & 15) * 4;
-    // Load i of 16 of token scale chunk c: rows 8 i .. 8 i + 7 (words past a row's end: its last).
-    auto ts_row = [&](int i) { return s_row[i * 8 + (ln >> 3)]; };
-    auto issue_ts = [&](int c, int i, uint32_t row) {
-      const int n = min(c * 8 + ((ln & 7) ^ (i & 7)), (ss >> 2) - 1);
-      g_load4(ascales, row + 4 * n, lds_ts + (c & 1) * (kGTsWords * 4) + i * 256);
-    };
-    // Stage kt0 mod 2 <- step kt0 (at most nk - 1), and load 2 (kt - 1) mod 16 + wave / 2 of the chunk after
-    // the one that step kt - 1 is in; `row` from ts_row(ts_load(kt)).
-    auto ts_load = [&](int kt) { return ((kt - 1) & 7) * 2 + (wave >> 1); };
-    auto issue = [&](int kt0, uint32_t row, auto h_tag) {
-      constexpr int hh = decltype(h_tag)::value;
-      const int kt = min(kt0, nk - 1);
-      const uint32_t st = lds_sm + (kt0 & 1) * kGStage;
-      const bool sh = half && kt == nk - 1;
-      const uint32_t oc = (sh ? ln & 31 : ln) * 16, osc = ows - (sh ? (ln & 8) * 4 : 0);
-      const uint8_t* const c0 = wcodes + (size_t)kt * 1024;
-      if (hh == 0) {
-        issue_ts(((kt0 - 1) >> 3) + 1, ts_load(kt0), row);
-        g_load4(wscales + (size_t)kt * 64, osc, st + wave * 256);
-      }
-#pragma unroll
-      for (int t = 0; t < 4; ++t)
-        if (hh == t / 2)
-          g_load16(acodes, min(oa[t] + (uint32_t)kt * 128, last_piece), st + kGTokAt + (4 * wave + t) * 1024);
-#pragma unroll
-      for (int s = 0; s < 4; ++s)
-        if (hh == s / 2)
-          g_load16(c0 + (s & 1) * strip + (s >> 1) * second, oc, st + kGCodeAt + (wave * 4 + s) * 1024);
-    };
-    using H0 = std::integral_constant<int, 0>;
-    using H1 = std::integral_constant<int, 1>;
-
-    // lane addresses of the operands: token pieces by half step and piece, codes, scales
     const int g = ln >> 5, i32 = ln & 31;
-    uint32_t at_tok[2][2];
-#pragma unroll
-    for (int kh = 0; kh < 2; ++kh)
-#pragma unroll
-      for (int c = 0; c < 2; ++c) at_tok[kh][c] = lds_sm + kGTokAt + i32 * 128 + ((4 * kh + 2 * c + g) ^ ((i32 >> 1) & 7)) * 16;
-    const uint32_t at_code = lds_sm + kGCodeAt + wave * 4096 + (i32 >> 4) * 1024 + g * 256 + (i32 & 15) * 16;
-    const uint32_t at_ws = lds_sm + wave * 256 + (i32 >> 4) * 64 + g * 16 + (i32 & 15);
-    const uint32_t at_ts = lds_ts + i32 * 32, x_ts = (i32 >> 3) * 4;
 
     f32x16 acc[2][4];
 #pragma unroll
@@ -307,17 +261,83 @@ void m8_tile(FfnArgs p, const uint8_t* ascales, uint32_t last_piece, uint8_t* hs
     };
     if (tid < kGM) s_row[tid] = row_at(min(tid, rows - 1)) * (uint32_t)ss;
     __syncthreads();
-#pragma unroll
-    for (int i = 0; i < 4; ++i) issue_ts(0, wave * 4 + i, ts_row(wave * 4 + i));
-    issue(0, ts_row(ts_load(0)), H0{}); issue(0, 0, H1{});
     // AM token tiles in NP pairs; a step has NQ = 2 NP parts, part q = pair q % NP of half q / NP
     auto run_k = [&](auto am_tag) {
       constexpr int AM = decltype(am_tag)::value, NP = (AM + 1) / 2, NQ = 2 * NP;
+      constexpr int NS = g_stages(AM), kStage = g_stage(AM), kLoads = 6 + AM;
+      int ln = lane;
+      asm volatile("; %1" : "+v"(ln) : "n"(AM));  // keeps the branches' own addresses out of what they share
+      const int g = ln >> 5, i32 = ln & 31;
+      const uint32_t lds_ts = lds_sm + NS * kStage;
+      auto stage = [&](int kt) { return lds_sm + (NS == 2 ? kt & 1 : kt % 3) * kStage; };
+      // A wave loads AM x 8 token rows (a lane's 16-byte piece permuted), the codes and the scales of
+      // its own four strips, and a load of the next token scale chunk: no branch, the same 6 + AM
+      // loads in each wave.  In a last step of 64 elements the second half of a code tile and of its
+      // scales does not exist (the first is read twice); the pieces of token rows past their end are
+      // other rows' or, at the buffer's last row, its last bytes.  None of that is used.
+      uint32_t oa[AM];
+#pragma unroll
+      for (int t = 0; t < AM; ++t) {
+        const int r = (AM * wave + t) * 8 + (ln >> 3);
+        oa[t] = row_at(min(r, rows - 1)) * (uint32_t)K + ((ln & 7) ^ ((r >> 1) & 7)) * 16;
+      }
+      // Load i of token scale chunk c: rows 8 i .. 8 i + 7 (words past a row's end: its last).
+      auto ts_row = [&](int i) { return s_row[i * 8 + (ln >> 3)]; };
+      auto issue_ts = [&](int c, int i, uint32_t row) {
+        const int n = min(c * 8 + ((ln & 7) ^ (i & 7)), (ss >> 2) - 1);
+        g_load4(ascales, row + 4 * n, lds_ts + (c & 1) * (32 * g_rows(AM)) + i * 256);
+      };
+      // Stage kt0 mod NS <- step kt0 (at most nk - 1), and a load of the token scale chunk after the
+      // one that step kt0 - NS + 1 is in (being read now): loads 2 n, 2 n + 1 with the n-th of the
+      // first 4 or 8 of its steps (all are there by its last but one), the first ones again after
+      // that.  `row` from ts_row(ts_load(kt0)).
+      auto ts_load = [&](int kt0) { return ((kt0 - NS + 1) & (g_rows(AM) / 16 - 1)) * 2 + (wave >> 1); };
+      auto issue = [&](int kt0, uint32_t row, auto h_tag) {
+        constexpr int hh = decltype(h_tag)::value;
+        const int kt = min(kt0, nk - 1);
+        const uint32_t st = stage(kt0);
+        const bool sh = half && kt == nk - 1;
+        const uint32_t oc = (sh ? ln & 31 : ln) * 16, osc = ows - (sh ? (ln & 8) * 4 : 0);
+        const uint8_t* const c0 = wcodes + (size_t)kt * 1024;
+        if (hh == 0) {
+          issue_ts(((kt0 - NS + 1) >> 3) + 1, ts_load(kt0), row);
+          g_load4(wscales + (size_t)kt * 64, osc, st + wave * 256);
+        }
+#pragma unroll
+        for (int t = 0; t < AM; ++t)
+          if (hh == t / 2)
+            g_load16(acodes, min(oa[t] + (uint32_t)kt * 128, last_piece), st + kGTokAt + (AM * wave + t) * 1024);
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+          if (hh == s / 2)
+            g_load16(c0 + (s & 1) * strip + (s >> 1) * second, oc, st + kGCodeAt + (wave * 4 + s) * 1024);
+      };
+      using H0 = std::integral_constant<int, 0>;
+      using H1 = std::integral_constant<int, 1>;
+      // lane addresses of the operands (in a stage): token pieces by half step and piece, codes, scales
+      uint32_t at_tok[2][2];
+#pragma unroll
+      for (int kh = 0; kh < 2; ++kh)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) at_tok[kh][c] = kGTokAt + i32 * 128 + ((4 * kh + 2 * c + g) ^ ((i32 >> 1) & 7)) * 16;
+      const uint32_t at_code = kGCodeAt + wave * 4096 + (i32 >> 4) * 1024 + g * 256 + (i32 & 15) * 16;
+      const uint32_t at_ws = wave * 256 + (i32 >> 4) * 64 + g * 16 + (i32 & 15);
+      const uint32_t at_ts = lds_ts + i32 * 32, x_ts = (i32 >> 3) * 4;
+#pragma unroll
+      for (int i = 0; i < g_rows(AM) / 32; ++i) {
+        const int l = wave * (g_rows(AM) / 32) + i;
+        issue_ts(0, l, ts_row(l));
+      }
+#pragma unroll
+      for (int i = 0; i < NS - 1; ++i) {
+        issue(i, ts_row(ts_load(i)), H0{});
+        issue(i, 0, H1{});
+      }
       Tokens tk[2];
       Weights wt[2];
       auto read = [&](int kt, auto q_tag) {
         constexpr int q = decltype(q_tag)::value, kh = q / NP, pr = q % NP;
-        const uint32_t st = (kt & 1) * kGStage;
+        const uint32_t st = stage(kt);
         if (pr == 0) {
 #pragma unroll
           for (int jn = 0; jn < 2; ++jn) {
@@ -326,7 +346,7 @@ void m8_tile(FfnArgs p, const uint8_t* ascales, uint32_t last_piece, uint8_t* hs
           }
         }
         // word of row r, step n of the chunk: n ^ (r / 8) mod 8, r = 32 it + i32
-        const uint32_t ts = at_ts + ((kt >> 3) & 1) * (kGTsWords * 4) + (((kt & 7) * 4) ^ x_ts);
+        const uint32_t ts = at_ts + ((kt >> 3) & 1) * (32 * g_rows(AM)) + (((kt & 7) * 4) ^ x_ts);
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           constexpr int it0 = 2 * pr;
@@ -376,20 +396,20 @@ void m8_tile(FfnArgs p, const uint8_t* ascales, uint32_t last_piece, uint8_t* hs
       using Q1 = std::integral_constant<int, 1 % NQ>;
       using Q2 = std::integral_constant<int, (NQ + 2) % NQ>;
       auto none = [] {};
-      g_wait_loads<0>();
+      g_wait_loads<(NS - 2) * kLoads>();
       lds_barrier();
-      issue(1, ts_row(ts_load(1)), H0{});
+      issue(NS - 1, ts_row(ts_load(NS - 1)), H0{});
       read(0, Q0{});
       for (int kt = 0; kt + 1 < nk; ++kt) {
-        const uint32_t row = ts_row(ts_load(kt + 2));
-        part(kt, Q0{}, [&] { issue(kt + 1, row, H1{}); });
+        const uint32_t row = ts_row(ts_load(kt + NS));
+        part(kt, Q0{}, [&] { issue(kt + NS - 1, row, H1{}); });
         if constexpr (NQ == 4) {
           part(kt, Q1{}, none);
           part(kt, Q2{}, none);
         }
-        g_wait_loads<0>();
+        g_wait_loads<(NS - 2) * kLoads>();
         lds_barrier();
-        part(kt + 1, QL{}, [&] { issue(kt + 2, row, H0{}); });
+        part(kt + 1, QL{}, [&] { issue(kt + NS, row, H0{}); });
       }
       part(nk - 1, Q0{}, none);
       blank(Q1{});
