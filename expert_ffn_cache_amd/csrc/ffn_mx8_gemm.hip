@@ -89,22 +89,31 @@ __device__ __forceinline__ void g_pair_rows(uint32_t (&w)[4]) {
 // first token tile of each XCD's share, and the token tiles in expert order.
 constexpr int kPlanShares = 256, kPlanTiles = 512;  // in words
 struct PlanTile {
-  int e, n0, rows, pad;  // expert, first grouped row, rows (at most kGM)
+  const uint8_t* w;  // the expert's entry
+  int n0, rows;      // first grouped row, rows (at most kGM)
 };
 __host__ __device__ constexpr int plan_counter(int mode, int xcd) { return 16 * (8 * mode + xcd); }
 
-// One workgroup: tiles and costs per expert and their prefixes (a thread an expert), then the
-// tiles (a thread a tile).  Shares are cut by cost, a tile's being its 32-row products and two for
+// One workgroup: entries, tiles and costs per expert and their prefixes (a thread an expert), then
+// the tiles (a thread a tile).  Shares are cut by cost, a tile's being its 32-row products and two for
 // what an item costs beside them.
 __device__ __forceinline__ int plan_cost(int rows) { return (rows + 31) / 32 + 2; }
 
 __global__ __launch_bounds__(kMaxE) void m8_plan(FfnArgs p, int* plan, int drawn) {
-  __shared__ int s_first[kMaxE + 1];
+  __shared__ int s_first[kMaxE + 1], s_n0[kMaxE], s_n[kMaxE];
   __shared__ long long s_before[kMaxE];
+  __shared__ const uint8_t* s_w[kMaxE];
   __shared__ int s_cnt[kMaxE / 64];
   __shared__ long long s_cost[kMaxE / 64];
-  const int e = threadIdx.x, lane = e & 63, wave = e >> 6;
-  const int n = e < p.E && active(p, e) ? p.offsets[e + 1] - p.offsets[e] : 0;
+  const int e = threadIdx.x, lane = e & 63, wave = e >> 6, nt = blockDim.x;  // E filled up to whole waves
+  const int at = min(e, p.E - 1), n0 = p.offsets[at], n1 = p.offsets[at + 1];
+  int n = n1 - n0;
+  if (e >= p.E || n <= 0 || n < p.nmin || n > p.nmax || (p.mask && !p.mask[e])) n = 0;
+  const uint8_t* const w = n ? (const uint8_t*)entry_of(p, e) : nullptr;
+  if (!w) n = 0;
+  s_w[e] = w;
+  s_n0[e] = n0;
+  s_n[e] = n;
   const int tiles = (n + kGM - 1) / kGM;
   const long long cost = tiles ? (long long)(tiles - 1) * plan_cost(kGM) + plan_cost(n - (tiles - 1) * kGM) : 0;
   int x = tiles;
@@ -126,33 +135,31 @@ __global__ __launch_bounds__(kMaxE) void m8_plan(FfnArgs p, int* plan, int drawn
   __syncthreads();
   int first = x - tiles, all = 0;
   long long before = y - cost, total = 0;
-#pragma unroll
-  for (int w = 0; w < kMaxE / 64; ++w) {
-    if (w < wave) {
-      first += s_cnt[w];
-      before += s_cost[w];
+  for (int i = 0; i < nt / 64; ++i) {
+    if (i < wave) {
+      first += s_cnt[i];
+      before += s_cost[i];
     }
-    all += s_cnt[w];
-    total += s_cost[w];
+    all += s_cnt[i];
+    total += s_cost[i];
   }
   s_first[e] = first;
   s_before[e] = before;
-  if (e == 0) s_first[kMaxE] = all;
+  if (e == 0) s_first[nt] = all;
   if (e <= 8) plan[kPlanShares + e] = e == 0 ? 0 : all;
   __syncthreads();
-  for (int m = threadIdx.x; m < all; m += kMaxE) {
-    int lo = 0, hi = kMaxE;  // the last expert whose first tile is not past m
+  for (int m = e; m < all; m += nt) {
+    int lo = 0, hi = nt;  // the last expert whose first tile is not past m
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
       if (s_first[mid] <= m) lo = mid; else hi = mid;
     }
-    const int i = m - s_first[lo], n0 = p.offsets[lo] + i * kGM;
-    const int rows = min(kGM, p.offsets[lo + 1] - n0);
-    ((PlanTile*)(plan + kPlanTiles))[m] = PlanTile{lo, n0, rows, 0};
-    const long long at = s_before[lo] + (long long)i * plan_cost(kGM);
+    const int i = m - s_first[lo], rows = min(kGM, s_n[lo] - i * kGM);
+    ((PlanTile*)(plan + kPlanTiles))[m] = PlanTile{s_w[lo], s_n0[lo] + i * kGM, rows};
+    const long long begins = s_before[lo] + (long long)i * plan_cost(kGM);
     for (int c = 1; c < 8; ++c) {  // the share that begins in this tile's cost begins with it
       const long long cut = total * c / 8;
-      if (cut >= at && cut < at + plan_cost(rows)) plan[kPlanShares + c] = m;
+      if (cut >= begins && cut < begins + plan_cost(rows)) plan[kPlanShares + c] = m;
     }
   }
 }
@@ -161,7 +168,7 @@ template <int MODE, int YDT>  // MODE 0: gate/up (h out), 1: down (y out)
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2)))
 void m8_tile(FfnArgs p, const uint8_t* ascales, uint32_t last_piece, uint8_t* hscales, int n_ntiles, int* plan) {
   __shared__ __attribute__((aligned(1024))) uint8_t sm[kGLds];
-  __shared__ int s_item[2];  // an XCD's share and the item in its queue, -1: none left
+  __shared__ int s_item[2][2];  // an XCD's share and the item in its queue: drawn there, taken elsewhere
   __shared__ uint32_t s_row[kGM];  // where the tile's token rows' scales start
 
   const int tid = threadIdx.x, lane = tid & 63;
@@ -177,70 +184,106 @@ void m8_tile(FfnArgs p, const uint8_t* ascales, uint32_t last_piece, uint8_t* hs
   // queue runs over its token tiles and, for each, over the weight tiles (2 to 16 token tiles to a
   // weight tile, for its codes to come from L2, are 0 to 5% slower at T = 8192: workgroups drift).
   // The next item is drawn while the current one is computed.
-  const int* const share = plan + kPlanShares;
+  __shared__ int share[9];  // first token tiles of the shares
+  if (tid < 9) share[tid] = plan[kPlanShares + tid];
+  __syncthreads();
   const PlanTile* const tiles = (const PlanTile*)(plan + kPlanTiles);
   auto share_items = [&](int q) { return (share[q + 1] - share[q]) * n_ntiles; };
   auto draw = [&](int q) { return atomicAdd(plan + plan_counter(MODE, q), 1); };
-  // Called by wave 0: item j of share q if there is one, else the next of the nearest share that
-  // has one left (all eight counters are looked at together).
-  auto settle = [&](int q, int j) {
-    if (j >= share_items(q)) {
-      const int c = ((int)blockIdx.x + lane) & 7, n = share_items(c);
-      for (;;) {
-        const bool left = lane < 8 && n > 0 &&
-            __hip_atomic_load(plan + plan_counter(MODE, c), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) < n;
-        const unsigned long long m = __ballot(left);
-        if (!m) {
-          q = -1;
-          break;
-        }
-        const int l = __ffsll((long long)m) - 1;
-        q = ((int)blockIdx.x + l) & 7;
-        j = 0;
-        if (lane == 0) j = draw(q);
-        j = __shfl(j, 0);
-        if (j < share_items(q)) break;
+  // Called by wave 0: an item of the nearest share that has one left (all eight counters are looked
+  // at together), -1 if there is none.
+  auto take = [&]() {
+    const int c = ((int)blockIdx.x + lane) & 7, n = share_items(c);
+    int q, j = 0;
+    for (;;) {
+      const bool left = lane < 8 && n > 0 &&
+          __hip_atomic_load(plan + plan_counter(MODE, c), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) < n;
+      const unsigned long long m = __ballot(left);
+      if (!m) {
+        q = -1;
+        break;
       }
+      const int l = __ffsll((long long)m) - 1;
+      q = ((int)blockIdx.x + l) & 7;
+      if (lane == 0) j = draw(q);
+      j = __shfl(j, 0);
+      if (j < share_items(q)) break;
     }
     if (lane == 0) {
-      s_item[0] = q;
-      s_item[1] = j;
+      s_item[1][0] = q;
+      s_item[1][1] = j;
     }
   };
-  // drawn ahead: held by lane 0 of wave 0
-  int next_q = 0, next_j = 0;
-  if (wave == 0) settle(blockIdx.x & 7, blockIdx.x >> 3);
-  __syncthreads();
+  int next_j = blockIdx.x >> 3;  // drawn ahead: held by thread 0
 
-  for (;;) {
-    const int q = s_item[0], j = s_item[1];
+  int ln0 = lane;
+  asm volatile("" : "+v"(ln0));  // keeps what follows from the lane out of the loops' live registers
+  // The item being loaded: its token tile and the wave's strips, 32 units of gate and of up, or 64
+  // output channels (past the matrix: the first ones, their results dropped).
+  const size_t strip = (size_t)K * 8, second = MODE == 0 ? fd / 2 : 2 * strip;
+  const uint32_t ows = ((ln0 >> 4) & 1) * (K / 2) + (ln0 >> 5) * (uint32_t)(MODE == 0 ? fd / 32 : K) + (ln0 & 15) * 4;
+  int q, n0, rows, r0;
+  bool out;
+  const uint8_t *wcodes, *wscales;
+  // Strips 2 h, 2 h + 1 of step kt0 (at most nk - 1) into the stage at st, with h = 0 the scales too.  In a
+  // last step of 64 elements the second half of a code tile and of its scales does not exist: the
+  // first is read twice and not used.
+  auto load_weights = [&](uint32_t st, int kt0, int h) {
+    const int kt = min(kt0, nk - 1);
+    const bool sh = half && kt == nk - 1;
+    if (h == 0) g_load4(wscales + (size_t)kt * 64, ows - (sh ? (ln0 & 8) * 4 : 0), st + wave * 256);
+    const uint8_t* const c0 = wcodes + (size_t)kt * 1024 + h * second;
+    const uint32_t oc = (sh ? ln0 & 31 : ln0) * 16;
+    g_load16(c0, oc, st + kGCodeAt + (wave * 4 + 2 * h) * 1024);
+    g_load16(c0 + strip, oc, st + kGCodeAt + (wave * 4 + 2 * h + 1) * 1024);
+  };
+  // Begins to load item s_item[from]: the token rows' numbers, into the last stage, and the weights of
+  // the first.
+  auto begin = [&](int from) {
+    q = __builtin_amdgcn_readfirstlane(s_item[from][0]);
+    const int j = __builtin_amdgcn_readfirstlane(s_item[from][1]);
     if (q < 0) return;
     const int m = j / n_ntiles, nt = j - m * n_ntiles;
-    const PlanTile tile = tiles[share[q] + m];
-    const int n0 = tile.n0, rows = tile.rows;
-    const uint8_t* W = (const uint8_t*)entry_of(p, tile.e);
-    __syncthreads();  // the item is read, and the previous one's readers of the LDS are done
-    next_q = q;
-    if (tid == 0) next_j = draw(q);
-    if (!W) {
-      if (wave == 0) settle(next_q, __shfl(next_j, 0));
-      __syncthreads();
-      continue;
+    const u32x4 t = *(const u32x4*)(tiles + share[q] + m);
+    n0 = __builtin_amdgcn_readfirstlane(t[2]);
+    rows = __builtin_amdgcn_readfirstlane(t[3]);
+    const uint8_t* const w = (const uint8_t*)((uint64_t)__builtin_amdgcn_readfirstlane(t[1]) << 32 |
+                                              (uint32_t)__builtin_amdgcn_readfirstlane(t[0]));
+    r0 = MODE == 0 ? nt * 128 + wave * 32 : nt * 256 + wave * 64;
+    out = r0 >= R;
+    const int rw = out ? 0 : r0;
+    wcodes = w + (MODE == 0 ? 0 : fd) + (size_t)rw * (K / 2);
+    wscales = w + 3 * (fd / 2) + (MODE == 0 ? 0 : 2 * (fd / 32)) + (size_t)rw * (K / 32);
+    if (MODE == 0) {
+      const uint32_t at = lds_sm + (rows <= 32 * kGFew ? (g_stages(1) - 1) * g_stage(1) : (g_stages(4) - 1) * g_stage(4));
+      g_load4(p.perm + n0, min(ln0, rows - 1) * 4, at);
+      g_load4(p.perm + n0, min(ln0 + 64, rows - 1) * 4, at + 256);
     }
-    int ln = lane;
-    asm volatile("" : "+v"(ln));  // keeps what follows from the lane out of the loops' live registers
+    load_weights(lds_sm, 0, 0);
+    load_weights(lds_sm, 0, 1);
+  };
+  // The item drawn from share c, if it is one, is begun before `meanwhile`; else one is taken elsewhere
+  // by wave 0 while the others run it.
+  auto next = [&](int c, auto meanwhile) {
+    if (tid == 0) {
+      s_item[0][0] = next_j < share_items(c) ? c : -1;
+      s_item[0][1] = next_j;
+    }
+    __syncthreads();  // and the previous item's readers of the LDS are done
+    begin(0);
+    const bool none = q < 0;
+    if (none && wave == 0) take();
+    meanwhile();
+    if (none) {
+      __syncthreads();
+      begin(1);
+    }
+  };
+  next(blockIdx.x & 7, [] {});
 
-    auto row_at = [&](int r) { return (uint32_t)(MODE == 0 ? p.perm[n0 + r] / p.k : n0 + r); };
-    // the wave's strips: 32 units of gate and of up, or 64 output channels (past the matrix:
-    // the first ones, their results dropped)
-    int r0 = MODE == 0 ? nt * 128 + wave * 32 : nt * 256 + wave * 64;
-    const bool out = r0 < R;
-    if (!out) r0 = 0;
-    const uint8_t* const wcodes = W + (MODE == 0 ? 0 : fd) + (size_t)r0 * (K / 2);
-    const uint8_t* const wscales = W + 3 * (fd / 2) + (MODE == 0 ? 0 : 2 * (fd / 32)) + (size_t)r0 * (K / 32);
-    const size_t strip = (size_t)K * 8, second = MODE == 0 ? fd / 2 : 2 * strip;
-    const uint32_t ows = ((ln >> 4) & 1) * (K / 2) + (ln >> 5) * (uint32_t)(MODE == 0 ? fd / 32 : K) + (ln & 15) * 4;
-    const int g = ln >> 5, i32 = ln & 31;
+  while (q >= 0) {
+    if (tid == 0) next_j = draw(q);
+    const int g = ln0 >> 5, i32 = ln0 & 31;
 
     f32x16 acc[2][4];
 #pragma unroll
@@ -259,58 +302,56 @@ void m8_tile(FfnArgs p, const uint8_t* ascales, uint32_t last_piece, uint8_t* hs
       u32x4 w[2];
       uint32_t s[2];
     };
-    if (tid < kGM) s_row[tid] = row_at(min(tid, rows - 1)) * (uint32_t)ss;
-    __syncthreads();
     // AM token tiles in NP pairs; a step has NQ = 2 NP parts, part q = pair q % NP of half q / NP
     auto run_k = [&](auto am_tag) {
       constexpr int AM = decltype(am_tag)::value, NP = (AM + 1) / 2, NQ = 2 * NP;
       constexpr int NS = g_stages(AM), kStage = g_stage(AM), kLoads = 6 + AM;
-      int ln = lane;
+      int ln = ln0;
       asm volatile("; %1" : "+v"(ln) : "n"(AM));  // keeps the branches' own addresses out of what they share
       const int g = ln >> 5, i32 = ln & 31;
       const uint32_t lds_ts = lds_sm + NS * kStage;
       auto stage = [&](int kt) { return lds_sm + (NS == 2 ? kt & 1 : kt % 3) * kStage; };
-      // A wave loads AM x 8 token rows (a lane's 16-byte piece permuted), the codes and the scales of
-      // its own four strips, and a load of the next token scale chunk: no branch, the same 6 + AM
-      // loads in each wave.  In a last step of 64 elements the second half of a code tile and of its
-      // scales does not exist (the first is read twice); the pieces of token rows past their end are
-      // other rows' or, at the buffer's last row, its last bytes.  None of that is used.
+      // Token rows of the tile: the wave loads AM x 8 of each step's (a lane's 16-byte piece permuted),
+      // and has every row's scales' offset in LDS (each wave writes them all, the same).  Rows past
+      // the tile's repeat its last; pieces past a row's end are other rows' or, at the buffer's last
+      // row, its last bytes, and are not used.
+      auto row_at = [&](int r) {
+        r = min(r, rows - 1);
+        return (uint32_t)(MODE == 0 ? g_lds<int>(lds_sm + (NS - 1) * kStage + r * 4, 0) / p.k : n0 + r);
+      };
+      if (MODE == 0) g_wait_loads<5>();
       uint32_t oa[AM];
 #pragma unroll
       for (int t = 0; t < AM; ++t) {
         const int r = (AM * wave + t) * 8 + (ln >> 3);
-        oa[t] = row_at(min(r, rows - 1)) * (uint32_t)K + ((ln & 7) ^ ((r >> 1) & 7)) * 16;
+        oa[t] = row_at(r) * (uint32_t)K + ((ln & 7) ^ ((r >> 1) & 7)) * 16;
       }
+#pragma unroll
+      for (int r = 0; r < g_rows(AM); r += 64) s_row[r + ln] = row_at(r + ln) * (uint32_t)ss;
       // Load i of token scale chunk c: rows 8 i .. 8 i + 7 (words past a row's end: its last).
       auto ts_row = [&](int i) { return s_row[i * 8 + (ln >> 3)]; };
       auto issue_ts = [&](int c, int i, uint32_t row) {
         const int n = min(c * 8 + ((ln & 7) ^ (i & 7)), (ss >> 2) - 1);
         g_load4(ascales, row + 4 * n, lds_ts + (c & 1) * (32 * g_rows(AM)) + i * 256);
       };
+      auto load_tokens = [&](uint32_t st, int kt0, int t) {
+        const int kt = min(kt0, nk - 1);
+        g_load16(acodes, min(oa[t] + (uint32_t)kt * 128, last_piece), st + kGTokAt + (AM * wave + t) * 1024);
+      };
       // Stage kt0 mod NS <- step kt0 (at most nk - 1), and a load of the token scale chunk after the
       // one that step kt0 - NS + 1 is in (being read now): loads 2 n, 2 n + 1 with the n-th of the
       // first 4 or 8 of its steps (all are there by its last but one), the first ones again after
-      // that.  `row` from ts_row(ts_load(kt0)).
+      // that.  `row` from ts_row(ts_load(kt0)).  No branch: 6 + AM loads in each wave, half of them
+      // with h_tag 0, half with 1.
       auto ts_load = [&](int kt0) { return ((kt0 - NS + 1) & (g_rows(AM) / 16 - 1)) * 2 + (wave >> 1); };
       auto issue = [&](int kt0, uint32_t row, auto h_tag) {
         constexpr int hh = decltype(h_tag)::value;
-        const int kt = min(kt0, nk - 1);
         const uint32_t st = stage(kt0);
-        const bool sh = half && kt == nk - 1;
-        const uint32_t oc = (sh ? ln & 31 : ln) * 16, osc = ows - (sh ? (ln & 8) * 4 : 0);
-        const uint8_t* const c0 = wcodes + (size_t)kt * 1024;
-        if (hh == 0) {
-          issue_ts(((kt0 - NS + 1) >> 3) + 1, ts_load(kt0), row);
-          g_load4(wscales + (size_t)kt * 64, osc, st + wave * 256);
-        }
+        if (hh == 0) issue_ts(((kt0 - NS + 1) >> 3) + 1, ts_load(kt0), row);
 #pragma unroll
         for (int t = 0; t < AM; ++t)
-          if (hh == t / 2)
-            g_load16(acodes, min(oa[t] + (uint32_t)kt * 128, last_piece), st + kGTokAt + (AM * wave + t) * 1024);
-#pragma unroll
-        for (int s = 0; s < 4; ++s)
-          if (hh == s / 2)
-            g_load16(c0 + (s & 1) * strip + (s >> 1) * second, oc, st + kGCodeAt + (wave * 4 + s) * 1024);
+          if (hh == t / 2) load_tokens(st, kt0, t);
+        load_weights(st, kt0, hh);
       };
       using H0 = std::integral_constant<int, 0>;
       using H1 = std::integral_constant<int, 1>;
@@ -330,8 +371,10 @@ void m8_tile(FfnArgs p, const uint8_t* ascales, uint32_t last_piece, uint8_t* hs
       }
 #pragma unroll
       for (int i = 0; i < NS - 1; ++i) {
-        issue(i, ts_row(ts_load(i)), H0{});
-        issue(i, 0, H1{});
+        if (i > 0) load_weights(stage(i), i, 0);
+        if (i > 0) load_weights(stage(i), i, 1);
+#pragma unroll
+        for (int t = 0; t < AM; ++t) load_tokens(stage(i), i, t);
       }
       Tokens tk[2];
       Weights wt[2];
@@ -396,7 +439,7 @@ void m8_tile(FfnArgs p, const uint8_t* ascales, uint32_t last_piece, uint8_t* hs
       using Q1 = std::integral_constant<int, 1 % NQ>;
       using Q2 = std::integral_constant<int, (NQ + 2) % NQ>;
       auto none = [] {};
-      g_wait_loads<(NS - 2) * kLoads>();
+      g_wait_loads<(NS - 2) * (5 + AM)>();
       lds_barrier();
       issue(NS - 1, ts_row(ts_load(NS - 1)), H0{});
       read(0, Q0{});
@@ -428,15 +471,16 @@ void m8_tile(FfnArgs p, const uint8_t* ascales, uint32_t last_piece, uint8_t* hs
       case 3: run_k(std::integral_constant<int, 3>{}); break;
       default: run_k(std::integral_constant<int, 4>{}); break;
     }
-    if (wave == 0) settle(next_q, __shfl(next_j, 0));
-
+    const int n0c = n0, rowsc = rows, r0c = r0;
+    const bool outc = out;
+    next(q, [&] {
     // lane 32 g + i, value v: token row i, weight row 8 (v / 4) + 4 g + v % 4 of the tile's 32
 #pragma unroll
     for (int it = 0; it < 4; ++it) {
-      if (it * 32 >= rows || !out) continue;
+      if (it * 32 >= rowsc || outc) continue;
       const int r = it * 32 + i32;
       if (MODE == 0) {
-        const int u0 = r0;
+        const int u0 = r0c;
         float h[16];
         uint32_t m = 0;
 #pragma unroll
@@ -451,17 +495,17 @@ void m8_tile(FfnArgs p, const uint8_t* ascales, uint32_t last_piece, uint8_t* hs
 #pragma unroll
         for (int b = 0; b < 4; ++b) w[b] = mxfp8_pack4(h[4 * b], h[4 * b + 1], h[4 * b + 2], h[4 * b + 3], s, sc);
         g_pair_rows(w);
-        if (r < rows) {
-          *(u32x4*)((uint8_t*)p.h + (size_t)(n0 + r) * p.f + u0 + 16 * g) = u32x4{w[0], w[1], w[2], w[3]};
-          if (g == 0) hscales[(size_t)(n0 + r) * mxfp8_scale_stride(p.f) + (u0 >> 5)] = (uint8_t)s;
+        if (r < rowsc) {
+          *(u32x4*)((uint8_t*)p.h + (size_t)(n0c + r) * p.f + u0 + 16 * g) = u32x4{w[0], w[1], w[2], w[3]};
+          if (g == 0) hscales[(size_t)(n0c + r) * mxfp8_scale_stride(p.f) + (u0 >> 5)] = (uint8_t)s;
         }
       } else {
 #pragma unroll
         for (int jn = 0; jn < 2; ++jn) {
-          const int o0 = r0 + jn * 32;
-          const size_t at = (size_t)(n0 + r) * p.d + o0;
+          const int o0 = r0c + jn * 32;
+          const size_t at = (size_t)(n0c + r) * p.d + o0;
           if (YDT == MOE_F32) {
-            if (r < rows) {
+            if (r < rowsc) {
 #pragma unroll
               for (int b = 0; b < 4; ++b)
                 *(f32x4*)((float*)p.y + at + 8 * b + 4 * g) = f32x4{acc[jn][it][4 * b], acc[jn][it][4 * b + 1],
@@ -476,7 +520,7 @@ void m8_tile(FfnArgs p, const uint8_t* ascales, uint32_t last_piece, uint8_t* hs
             }
             g_pair_rows(a);
             g_pair_rows(c);
-            if (r < rows) {
+            if (r < rowsc) {
               uint16_t* y = (uint16_t*)p.y + at + 16 * g;
               *(u32x4*)y = u32x4{a[0], c[0], a[1], c[1]};
               *(u32x4*)(y + 8) = u32x4{a[2], c[2], a[3], c[3]};
@@ -485,7 +529,7 @@ void m8_tile(FfnArgs p, const uint8_t* ascales, uint32_t last_piece, uint8_t* hs
         }
       }
     }
-    __syncthreads();  // the next item is there
+    });
   }
 }
 
@@ -509,7 +553,7 @@ int launch_ffn_mx8_gemm(const FfnArgs& p, int T, int y_dtype, hipStream_t stream
   const dim3 grid((num_cus() * 2 + 7) / 8 * 8), blk(256);
   const int ntd = (p.d + 255) / 256;
   const uint32_t last_x = (uint32_t)((size_t)T * p.d - 16), last_h = (uint32_t)(A * p.f - 16);
-  hipLaunchKernelGGL(m8_plan, dim3(1), dim3(kMaxE), 0, stream, p, plan, (int)grid.x / 8);
+  hipLaunchKernelGGL(m8_plan, dim3(1), dim3((p.E + 63) / 64 * 64), 0, stream, p, plan, (int)grid.x / 8);
   MOE_LAUNCH_CHECK();
   hipLaunchKernelGGL((m8_tile<0, MOE_BF16>), grid, blk, 0, stream, p, xs, last_x, hs, (p.f + 127) / 128, plan);
   MOE_LAUNCH_CHECK();
