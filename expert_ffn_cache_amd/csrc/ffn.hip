@@ -16,6 +16,9 @@
 //  * MXFP4 weights (bf16 activations): codes expanded to bf16 in registers and multiplied
 //    on the matrix cores against staged token rows: weight streaming for decode-shaped
 //    counts (ffn_mx.hip), a grouped GEMM for prefill-shaped ones (ffn_mx_gemm.hip).
+//  * MXFP4 weights with MXFP8 activations: codes and scales of both sides to the block-scaled
+//    matrix instructions, h in MXFP8: weight streaming up to 32 tokens (ffn_mx8.hip), a
+//    grouped GEMM above (ffn_mx8_gemm.hip).
 // Both bf16 paths fuse SiLU(g)*u into the gate/up epilogue and write h once as bf16.
 #include <algorithm>
 #include <mutex>
@@ -42,15 +45,17 @@ constexpr int kMxMaxRows = 16;
 // (T*k / E), MXFP4 experts above kMxGemmMinRowsPerExpert (their streaming path, with the row
 // split above, stays ahead to about 5 rows per expert at Zipf 0.2 and beyond 8 when skewed).
 constexpr long long kGemmMinRowsPerExpert = 2, kMxGemmMinRowsPerExpert = 8;
-// MXFP8 activations: weight streaming for every expert up to kMx8MaxT tokens, the grouped GEMM
-// above 3 rows per expert on average, between them a split at kMx8MaxRows rows (what one pass of
-// the streaming kernels takes).  d = 4096, f = 2048, top 6 of 256, streaming | split | GEMM in us at
-// Zipf 0.2: T = 32 264 | 272 | 294; T = 64 371 | 381 | 416; T = 128 473 | 488 | 541; T = 170 507 | 524 |
-// 558; at Zipf 1: T = 32 85 | 95 | 85; T = 64 139 | 148 | 133; T = 128 270 | 187 | 149; T = 170 372 | 198
-// | 163.  A split pays the GEMM's launches (about 9 us) where no expert has more rows, and its
-// latency where few do; no split leaves skewed calls at up to twice the time.
-constexpr long long kMx8GemmMinRowsPerExpert = 3;
-constexpr int kMx8MaxT = 32, kMx8MaxRows = 32;
+// MXFP8 activations: weight streaming up to kMx8MaxT tokens (what one pass of its kernels takes, and
+// no expert has more rows) and up to twice that (two passes at most) while the experts have at most
+// kMx8FewRows rows on average; the grouped GEMM above.  Streaming | GEMM in us, Zipf 0.2:
+//   d = 4096, f = 2048, top 6 of 256:  T = 8 95 | 117   T = 32 265 | 285  T = 64 373 | 390   T = 128 480 | 505
+//   d = 2048, f = 768, top 8 of 128:   T = 8 28 | 33    T = 32 59 | 63    T = 64 67 | 71     T = 128 75 | 73
+//   d = 4096, f = 2048, top 2 of 8:    T = 8 24 | 34    T = 32 29 | 34    T = 64 37 | 34     T = 128 61 | 40
+//   one expert:                        T = 8 17 | 32    T = 32 31 | 33    T = 64 57 | 40     T = 128 105 | 54
+// and where hot experts take several passes, top 6 of 256: Zipf 0.5, T = 64 233 | 232; Zipf 1, T = 32 85 | 78,
+// T = 64 140 | 107, T = 128 270 | 134.  The rows do not split between the two: the second set of
+// launches costs what it gains (T = 64 377 and 127 us).
+constexpr int kMx8MaxT = 32, kMx8FewRows = 2;
 constexpr int kMx8MaxDim = 0x7FFFFFFF - 127;  // element numbers to the end of a row's last tile are ints
 // Rounds of resident workgroups in the row-split dot-product launches (each loops over items).
 constexpr int kDotSplitRounds = 2;
@@ -169,17 +174,11 @@ extern "C" int moe_expert_ffn(const void* x, int act_dtype, const int32_t* perm,
     MOE_LAUNCH_CHECK();
     return MOE_OK;
   }
-  if (act_dtype == MOE_MXFP8) {  // as below, with kernels and thresholds of its own
-    const int A = T * k, experts = std::min(E, A);
-    const bool gemm = path == MOE_PATH_GEMM || (path == MOE_PATH_AUTO && (long long)T * k > kMx8GemmMinRowsPerExpert * E);
-    if (gemm && mx8_gemm_fits) return launch_ffn_mx8_gemm(p, T, y_dtype, stream);
-    if (path == MOE_PATH_GEMV || T <= kMx8MaxT || !mx8_gemm_fits) return launch_ffn_mx8(p, T, y_dtype, stream, experts);
-    FfnArgs few = p, many = p;
-    few.nmax = kMx8MaxRows;
-    many.nmin = kMx8MaxRows + 1;
-    int rc = launch_ffn_mx8(few, T, y_dtype, stream, experts);
-    if (rc == MOE_OK) rc = launch_ffn_mx8_gemm(many, T, y_dtype, stream);
-    return rc;
+  if (act_dtype == MOE_MXFP8) {
+    const bool few = T <= kMx8MaxT || (T <= 2 * kMx8MaxT && T * k <= kMx8FewRows * E);
+    if (mx8_gemm_fits && (path == MOE_PATH_GEMM || (path == MOE_PATH_AUTO && !few)))
+      return launch_ffn_mx8_gemm(p, T, y_dtype, stream);
+    return launch_ffn_mx8(p, T, y_dtype, stream, std::min(E, T * k));
   }
   if (mx) {
     const bool gemm = path == MOE_PATH_GEMM ||

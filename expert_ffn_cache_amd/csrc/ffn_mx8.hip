@@ -60,7 +60,7 @@ __device__ __forceinline__ M8Item m8_item(const FfnArgs& p, int a) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int n = hi[j] - lo[j];
-      const bool act = e0 + 64 * j + lane < p.E && n > 0 && n >= p.nmin && n <= p.nmax && on[j];
+      const bool act = e0 + 64 * j + lane < p.E && n > 0 && on[j];
       const unsigned long long m = __ballot(act);
       const int c = __popcll(m);
       if (a < seen + c) {

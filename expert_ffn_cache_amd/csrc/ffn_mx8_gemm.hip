@@ -108,7 +108,7 @@ __global__ __launch_bounds__(kMaxE) void m8_plan(FfnArgs p, int* plan, int drawn
   const int e = threadIdx.x, lane = e & 63, wave = e >> 6, nt = blockDim.x;  // E filled up to whole waves
   const int at = min(e, p.E - 1), n0 = p.offsets[at], n1 = p.offsets[at + 1];
   int n = n1 - n0;
-  if (e >= p.E || n <= 0 || n < p.nmin || n > p.nmax || (p.mask && !p.mask[e])) n = 0;
+  if (e >= p.E || n < 0 || (p.mask && !p.mask[e])) n = 0;
   const uint8_t* const w = n ? (const uint8_t*)entry_of(p, e) : nullptr;
   if (!w) n = 0;
   s_w[e] = w;
