@@ -31,13 +31,23 @@ def _tdtype(code):
     return torch.float32 if code == MOE_F32 else torch.bfloat16
 
 
-def _code(t):
-    """MOE_* code of a tensor's (or no tensor's) element type."""
+def _code(t, n):
+    """MOE_* code of the element type of a contiguous tensor of n elements (or of no tensor)."""
     if t is None:
         return MOE_BF16
     if t.dtype not in (torch.float32, torch.bfloat16):
         raise TypeError(f"fp32 or bf16 tensor expected, got {t.dtype}")
+    if t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"contiguous tensor of {n} elements expected, got {tuple(t.shape)}, strides {t.stride()}")
     return MOE_F32 if t.dtype == torch.float32 else MOE_BF16
+
+
+def _check_bytes(t, n):
+    """MXFP8 rows: a contiguous uint8 tensor of at least n bytes."""
+    if t.dtype != torch.uint8:
+        raise TypeError(f"uint8 tensor of MXFP8 rows expected, got {t.dtype}")
+    if t.numel() < n or not t.is_contiguous():
+        raise ValueError(f"contiguous tensor of at least {n} bytes expected, got {tuple(t.shape)}, strides {t.stride()}")
 
 
 class MoeLayer:
@@ -90,6 +100,8 @@ class MoeLayer:
 
     def ffn(self, x, arena, entry_stride, expert_slot=None, mask=None, slot_key=None, key_base=0,
             path=MOE_PATH_AUTO, stream=None):
+        if self.dtype == MOE_MXFP8 and torch.is_tensor(x):
+            _check_bytes(x, moe_mxfp8_bytes(self.T, self.d))
         moe_expert_ffn(x, self.dtype, self.perm, self.offsets, self.T, self.k, self.E, self.d,
                        self.f, expert_slot, arena, entry_stride, self.w_dtype, mask, slot_key,
                        key_base, self.ffn_ws, self.ffn_ws_bytes, self.y_perm, self.y_dtype, path,
@@ -97,20 +109,28 @@ class MoeLayer:
 
     def quantize(self, x, stream=None):
         """x [T, d] (fp32 or bf16) into the layer's MXFP8 rows."""
-        moe_mxfp8_quantize(x, _code(x), self.T, self.d, self.x8, stream)
+        moe_mxfp8_quantize(x, _code(x, self.T * self.d), self.T, self.d, self.x8, stream)
         return self.x8
 
     def norm(self, x, gamma, eps, delta=None, x_out=None, y=None, stream=None):
         """Residual addition and RMS norm in front of the layer: x (+ delta) to x_out, the
         normalised rows to y and, with MXFP8 activations, to the layer's MXFP8 rows."""
-        moe_rmsnorm(x, _code(x), delta, _code(delta), gamma, _code(gamma), eps, self.T, self.d, x_out,
-                    y, _code(y), self.x8 if self.dtype == MOE_MXFP8 else None, stream)
+        n = self.T * self.d
+        if x_out is not None and _code(x_out, n) != _code(x, n):
+            raise TypeError(f"x_out is {x_out.dtype}, x {x.dtype}")
+        moe_rmsnorm(x, _code(x, n), delta, _code(delta, n), gamma, _code(gamma, self.d), eps, self.T, self.d,
+                    x_out, y, _code(y, n), self.x8 if self.dtype == MOE_MXFP8 else None, stream)
 
     def combine_norm(self, x, gamma, eps, x_out=None, y=None, x8=None, stream=None):
         """combine(), the residual addition and the next RMS norm in one launch (self.out is not
         written): x + combined rows to x_out, the normalised rows to y and / or, in MXFP8, to x8."""
-        moe_combine_rmsnorm(self.y_perm, self.y_dtype, self.inv, self.w, self.k, x, _code(x), gamma,
-                            _code(gamma), eps, self.T, self.d, x_out, y, _code(y), x8, stream)
+        n = self.T * self.d
+        if x_out is not None and _code(x_out, n) != _code(x, n):
+            raise TypeError(f"x_out is {x_out.dtype}, x {x.dtype}")
+        if x8 is not None:
+            _check_bytes(x8, moe_mxfp8_bytes(self.T, self.d))
+        moe_combine_rmsnorm(self.y_perm, self.y_dtype, self.inv, self.w, self.k, x, _code(x, n), gamma,
+                            _code(gamma, self.d), eps, self.T, self.d, x_out, y, _code(y, n), x8, stream)
 
     def combine(self, stream=None):
         moe_combine(self.y_perm, self.y_dtype, self.inv, self.w, self.T, self.k, self.d,

@@ -4,6 +4,7 @@ import numpy as np
 import pytest
 
 import expert_ffn_cache_amd as moe
+from expert_ffn_cache_amd.layer import MoeLayer
 from oracle import mx8
 
 
@@ -171,3 +172,22 @@ def test_expert_ffn_with_mxfp8_activations_refuses():
     T = moe.moe_expert_ffn_noalloc_max_bytes() // (2048 + 64) + 1
     na = [A, X8, A, A, T, 1, 256, 4096, 2048, None, A, eb, X4, None, None, 0, A, F32, 0, None, None]
     assert moe.lib().moe_expert_ffn_noalloc(*na) == moe.MOE_ETOOBIG
+
+
+def test_layer_refuses_tensors_that_do_not_fit():
+    torch = pytest.importorskip("torch")
+    layer = MoeLayer(4, 8, 2, 128, 64, dtype=X8, device="cpu")
+    x, g = torch.zeros(4, 128, dtype=torch.bfloat16), torch.zeros(128)
+    wide = torch.zeros(4, 256, dtype=torch.bfloat16)[:, :128]
+    for call in (lambda: layer.quantize(wide), lambda: layer.quantize(x[:3]), lambda: layer.norm(wide, g, 1e-6),
+                 lambda: layer.norm(x, g[:64], 1e-6), lambda: layer.norm(x, g, 1e-6, delta=wide),
+                 lambda: layer.norm(x, g, 1e-6, x_out=wide), lambda: layer.norm(x, g, 1e-6, y=x[:2]),
+                 lambda: layer.combine_norm(wide, g, 1e-6, y=x), lambda: layer.combine_norm(x, g, 1e-6, y=wide),
+                 lambda: layer.combine_norm(x, g, 1e-6, x8=layer.x8[:-1]), lambda: layer.ffn(layer.x8[:-1], None, 0)):
+        with pytest.raises(ValueError):
+            call()
+    for call in (lambda: layer.quantize(x.half()), lambda: layer.norm(x, g, 1e-6, x_out=x.float()),
+                 lambda: layer.combine_norm(x.float(), g, 1e-6, x_out=x), lambda: layer.combine_norm(x, g, 1e-6, x8=x),
+                 lambda: layer.ffn(x, None, 0)):
+        with pytest.raises(TypeError):
+            call()
