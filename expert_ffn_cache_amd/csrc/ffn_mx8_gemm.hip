@@ -102,7 +102,7 @@ __device__ __forceinline__ void g_pair_rows(uint32_t (&w)[4]) {
 }
 
 // The plan of a call, in its workspace: a queue counter per mode and XCD (64 bytes apart), the
-// first token tile of each XCD's share, and the token tiles in expert order.
+// first token tile of each XCD's share, and the token tiles.
 constexpr int kPlanShares = 256, kPlanTiles = 512;  // in words
 struct PlanTile {
   const uint8_t* w;  // the expert's entry
@@ -111,16 +111,19 @@ struct PlanTile {
 __host__ __device__ constexpr int plan_counter(int mode, int xcd) { return 16 * (8 * mode + xcd); }
 
 // One workgroup: entries, tiles and costs per expert and their prefixes (a thread an expert), then
-// the tiles (a thread a tile).  Shares are cut by cost, a tile's being its 32-row products and two for
-// what an item costs beside them.
-__device__ __forceinline__ int plan_cost(int rows) { return (rows + 31) / 32 + 2; }
+// the tiles (a thread a tile): those of experts with more than 32 kGFew rows first, whose items take
+// longest, so that the last round is of short ones and workgroups of an XCD keep step (d = 2048,
+// f = 768, top 8 of 128, Zipf 1, T = 333 and 100: 70 and 48 us, in plain expert order 74 and 50; both
+// kinds in every share 75 and 52).  Shares are cut by cost, a tile's being its 32-row products and
+// four for what an item costs beside them.
+__device__ __forceinline__ int plan_cost(int rows) { return (rows + 31) / 32 + 4; }
 
 __global__ __launch_bounds__(kMaxE) void m8_plan(FfnArgs p, int* plan, int drawn) {
-  __shared__ int s_first[kMaxE + 1], s_n0[kMaxE], s_n[kMaxE];
-  __shared__ long long s_before[kMaxE];
+  __shared__ int s_first[2][kMaxE], s_n0[kMaxE], s_n[kMaxE];
+  __shared__ long long s_before[2][kMaxE];
   __shared__ const uint8_t* s_w[kMaxE];
-  __shared__ int s_cnt[kMaxE / 64];
-  __shared__ long long s_cost[kMaxE / 64];
+  __shared__ int s_cnt[2][kMaxE / 64];
+  __shared__ long long s_cost[2][kMaxE / 64];
   const int e = threadIdx.x, lane = e & 63, wave = e >> 6, nt = blockDim.x;  // E filled up to whole waves
   const int at = min(e, p.E - 1), n0 = p.offsets[at], n1 = p.offsets[at + 1];
   int n = n1 - n0;
@@ -132,47 +135,61 @@ __global__ __launch_bounds__(kMaxE) void m8_plan(FfnArgs p, int* plan, int drawn
   s_n[e] = n;
   const int tiles = (n + kGM - 1) / kGM;
   const long long cost = tiles ? (long long)(tiles - 1) * plan_cost(kGM) + plan_cost(n - (tiles - 1) * kGM) : 0;
-  int x = tiles;
-  long long y = cost;
+  const int few = n <= 32 * kGFew;
+  int x[2] = {few ? 0 : tiles, few ? tiles : 0};
+  long long y[2] = {few ? 0 : cost, few ? cost : 0};
 #pragma unroll
-  for (int off = 1; off < 64; off <<= 1) {
-    const int u = __shfl_up(x, off);
-    const long long v = __shfl_up(y, off);
-    if (lane >= off) {
-      x += u;
-      y += v;
+  for (int c = 0; c < 2; ++c) {
+    const int x0 = x[c];
+    const long long y0 = y[c];
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+      const int u = __shfl_up(x[c], off);
+      const long long v = __shfl_up(y[c], off);
+      if (lane >= off) {
+        x[c] += u;
+        y[c] += v;
+      }
     }
-  }
-  if (lane == 63) {
-    s_cnt[wave] = x;
-    s_cost[wave] = y;
+    if (lane == 63) {
+      s_cnt[c][wave] = x[c];
+      s_cost[c][wave] = y[c];
+    }
+    x[c] -= x0;
+    y[c] -= y0;
   }
   if (e < 16) plan[16 * e] = drawn;  // every workgroup begins with the item of its place in its XCD
   __syncthreads();
-  int first = x - tiles, all = 0;
-  long long before = y - cost, total = 0;
-  for (int i = 0; i < nt / 64; ++i) {
-    if (i < wave) {
-      first += s_cnt[i];
-      before += s_cost[i];
+  int all = 0, many = 0;
+  long long total = 0;
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    x[c] += all;
+    y[c] += total;
+    for (int i = 0; i < nt / 64; ++i) {
+      if (i < wave) {
+        x[c] += s_cnt[c][i];
+        y[c] += s_cost[c][i];
+      }
+      all += s_cnt[c][i];
+      total += s_cost[c][i];
     }
-    all += s_cnt[i];
-    total += s_cost[i];
+    s_first[c][e] = x[c];
+    s_before[c][e] = y[c];
+    if (c == 0) many = all;
   }
-  s_first[e] = first;
-  s_before[e] = before;
-  if (e == 0) s_first[nt] = all;
   if (e <= 8) plan[kPlanShares + e] = e == 0 ? 0 : all;
   __syncthreads();
   for (int m = e; m < all; m += nt) {
+    const int few_tile = m >= many;
     int lo = 0, hi = nt;  // the last expert whose first tile is not past m
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (s_first[mid] <= m) lo = mid; else hi = mid;
+      if (s_first[few_tile][mid] <= m) lo = mid; else hi = mid;
     }
-    const int i = m - s_first[lo], rows = min(kGM, s_n[lo] - i * kGM);
+    const int i = m - s_first[few_tile][lo], rows = min(kGM, s_n[lo] - i * kGM);
     ((PlanTile*)(plan + kPlanTiles))[m] = PlanTile{s_w[lo], s_n0[lo] + i * kGM, rows};
-    const long long begins = s_before[lo] + (long long)i * plan_cost(kGM);
+    const long long begins = s_before[few_tile][lo] + (long long)i * plan_cost(kGM);
     for (int c = 1; c < 8; ++c) {  // the share that begins in this tile's cost begins with it
       const long long cut = total * c / 8;
       if (cut >= begins && cut < begins + plan_cost(rows)) plan[kPlanShares + c] = m;
