@@ -47,15 +47,19 @@ constexpr int kMxMaxRows = 16;
 constexpr long long kGemmMinRowsPerExpert = 2, kMxGemmMinRowsPerExpert = 8;
 // MXFP8 activations: weight streaming up to kMx8MaxT tokens (what one pass of its kernels takes, and
 // no expert has more rows) and up to twice that (two passes at most) while the experts have at most
-// kMx8FewRows rows on average; the grouped GEMM above.  Streaming | GEMM in us, Zipf 0.2:
+// kMx8FewRows rows on average or at most kMx8Small weights a matrix (a second pass then costs less
+// than the GEMM's third launch and its start); the grouped GEMM above.  Streaming | GEMM in us, Zipf 0.2:
 //   d = 4096, f = 2048, top 6 of 256:  T = 8 95 | 117   T = 32 265 | 285  T = 64 373 | 390   T = 128 480 | 505
 //   d = 2048, f = 768, top 8 of 128:   T = 8 28 | 33    T = 32 59 | 63    T = 64 67 | 71     T = 128 75 | 73
 //   d = 4096, f = 2048, top 2 of 8:    T = 8 24 | 34    T = 32 29 | 34    T = 64 37 | 34     T = 128 61 | 40
 //   one expert:                        T = 8 17 | 32    T = 32 31 | 33    T = 64 57 | 40     T = 128 105 | 54
+//   d = 1024, f = 512, Zipf 0.5, top 2 of 8: T = 40 13 | 18, T = 64 17 | 21, T = 100 22 | 21; top 4 of 64: T = 40 17 | 20,
+//   T = 64 18 | 21, T = 100 25 | 23; d = 2048, f = 1024, top 3 of 200: T = 40 36 | 38, T = 64 44 | 40
 // and where hot experts take several passes, top 6 of 256: Zipf 0.5, T = 64 233 | 232; Zipf 1, T = 32 85 | 78,
 // T = 64 140 | 107, T = 128 270 | 134.  The rows do not split between the two: the second set of
 // launches costs what it gains (T = 64 377 and 127 us).
 constexpr int kMx8MaxT = 32, kMx8FewRows = 2;
+constexpr long long kMx8Small = 1 << 19;
 constexpr int kMx8MaxDim = 0x7FFFFFFF - 127;  // element numbers to the end of a row's last tile are ints
 // Rounds of resident workgroups in the row-split dot-product launches (each loops over items).
 constexpr int kDotSplitRounds = 2;
@@ -175,7 +179,7 @@ extern "C" int moe_expert_ffn(const void* x, int act_dtype, const int32_t* perm,
     return MOE_OK;
   }
   if (act_dtype == MOE_MXFP8) {
-    const bool few = T <= kMx8MaxT || (T <= 2 * kMx8MaxT && T * k <= kMx8FewRows * E);
+    const bool few = T <= kMx8MaxT || (T <= 2 * kMx8MaxT && (T * k <= kMx8FewRows * E || (long long)d * f <= kMx8Small));
     if (mx8_gemm_fits && (path == MOE_PATH_GEMM || (path == MOE_PATH_AUTO && !few)))
       return launch_ffn_mx8_gemm(p, T, y_dtype, stream);
     return launch_ffn_mx8(p, T, y_dtype, stream, std::min(E, T * k));
