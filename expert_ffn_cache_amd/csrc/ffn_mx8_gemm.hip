@@ -28,9 +28,10 @@
 // PFLOP/s) and 1.24 ms at Zipf 1, matrix pipes busy 65% of the cycles at a clock that the power
 // limit holds near 1.65 GHz (all-zero operands, the same instructions at a higher clock: 18%
 // less time); T = 512 0.60 ms, 5.7 TB/s of weights.  Measured against it, T = 8192: one workgroup of
-// 8 waves and 256 token rows with three stages 3% slower, of 4 waves with 128 x 128 results each 8%
-// slower; weight codes straight to registers 1% slower; token tiles of even size, or those of an
-// expert side by side at each weight tile, the same.
+// 8 waves and 256 token rows with three stages 3% slower (an earlier form of both), of 4 waves with 128 x
+// 128 results each 8% slower; weight codes straight to registers 1% slower; four half steps in the
+// ring 7% slower; token tiles of even size, or those of an expert side by side at each weight
+// tile, the same.
 //
 // Work list: a small kernel lists the experts' token tiles from the offsets and cuts the list into a
 // share for each XCD; persistent workgroups draw (token tile, weight tile) items from their XCD's
